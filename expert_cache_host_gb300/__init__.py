@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_PKG, "_build", "libftmoe.so")
 
 FT_OK, FT_E_ARG, FT_E_PIN, FT_E_NOMEM, FT_E_CUDA, FT_E_STATE, FT_E_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 FT_ST_ROUTE_RANGE, FT_ST_NAN, FT_ST_CLOCK_WRAP, FT_ST_BAD_SLOT = 1, 2, 4, 8
-FT_DTYPE_BF16, FT_DTYPE_MXFP4 = 0, 1
+FT_ST_TIMEOUT, FT_ST_NO_ROOM, FT_ST_BAD_TREE, FT_ST_BAD_TOKEN = 16, 32, 64, 128
+FT_DTYPE_BF16, FT_DTYPE_MXFP4, FT_DTYPE_F16, FT_DTYPE_F32 = 0, 1, 2, 3
 FT_DECODE_CACHED, FT_PREFILL_LAYER = 0, 1
 FT_FILL_KERNEL, FT_FILL_COPY_ENGINE = 0, 1
 FT_FILL_ORDER_ID, FT_FILL_ORDER_MOST_ROUTED = 0, 1
@@ -34,6 +35,7 @@ EXPORTS = (
     "ft_cache_rebuild_retain", "ft_cpu_executor", "ft_cpu_experts",
     "ft_ratio_adapter_init", "ft_ratio_adapter_update", "ft_report_host_rate", "ft_measured_bandwidths",
     "ft_adapt_ratio", "ft_decode_meters", "ft_decode_path",
+    "ft_kv_plan", "ft_qk_norm_rope", "ft_tree_attention", "ft_tree_attention_workspace", "ft_token_logprobs",
     "ft_last_error",
 )
 FT_K_ROUTE, FT_K_CONTROL, FT_K_FILL, FT_K_EXPERTS, FT_K_MERGE, FT_K_UPLOAD, FT_K_PREFILL, FT_K_GEMM, FT_K_CPU = range(9)
@@ -67,6 +69,42 @@ class ft_ratio_adapter(ctypes.Structure):
 class ft_step_out(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "ids", "weights", "slot_ids", "uniq", "hit_list", "fetch", "victims", "evicted", "cpu_list", "counts")]
+
+
+def _fields(ctype, names: str):
+    return [(n, ctype) for n in names.split()]
+
+
+class ft_kv_cache(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "k v") +
+                _fields(ctypes.c_int32, "dtype num_pages page_size kv_heads head_dim reserved") +
+                _fields(ctypes.c_int64, "k_page_stride k_token_stride k_head_stride "
+                                        "v_page_stride v_token_stride v_head_stride"))
+
+
+class ft_plan_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "ctx_len new_len parents free_pages free_count block_table q_start slots "
+                                         "positions mask free_left status") +
+                _fields(ctypes.c_int32, "num_reqs page_size table_width max_tokens mask_words reserved"))
+
+
+class ft_qk_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "q k v q_weight k_weight cos_sin positions slots q_out status") +
+                _fields(ctypes.c_int64, "q_stride k_stride v_stride q_out_stride") +
+                _fields(ctypes.c_int32, "T q_heads rot_dim max_pos interleaved") +
+                [("eps", ctypes.c_float), ("cache", ft_kv_cache)])
+
+
+class ft_attn_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "q out lse q_start ctx_len block_table mask workspace status") +
+                _fields(ctypes.c_int64, "q_stride out_stride") + _fields(ctypes.c_uint64, "workspace_bytes") +
+                _fields(ctypes.c_int32, "max_tokens num_reqs q_heads table_width mask_words") +
+                [("scale", ctypes.c_float), ("cache", ft_kv_cache)])
+
+
+class ft_logprob_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "logits tokens logprob entropy top_ids top_logprobs status") +
+                _fields(ctypes.c_int64, "row_stride") + _fields(ctypes.c_int32, "dtype T V top_n"))
 
 
 _lib = None
@@ -114,6 +152,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "ft_adapt_ratio": ([vp, ctypes.POINTER(ft_ratio_adapter), vp, vp], i32),
             "ft_decode_meters": ([vp, vp, i32], i32),
             "ft_decode_path": ([vp], i32),
+            "ft_kv_plan": ([ctypes.POINTER(ft_plan_args), vp], i32),
+            "ft_qk_norm_rope": ([ctypes.POINTER(ft_qk_args), vp], i32),
+            "ft_tree_attention": ([ctypes.POINTER(ft_attn_args), vp], i32),
+            "ft_tree_attention_workspace": ([ctypes.POINTER(ft_attn_args), ctypes.POINTER(ctypes.c_uint64)], i32),
+            "ft_token_logprobs": ([ctypes.POINTER(ft_logprob_args), vp], i32),
             "ft_last_error": ([], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -320,6 +363,63 @@ def ft_decode_experts_noalloc(arena_ptr: int, num_slots: int, hidden: int, inter
     _chk(load().ft_decode_experts_noalloc(v(arena_ptr), num_slots, hidden, inter, top_k, T, v(slot_ids_ptr),
                                           v(weights_ptr), v(hidden_ptr), v(partial_ptr or None), v(out_ptr),
                                           v(status_ptr or None), v(stream)))
+
+
+def _args(struct, kw):
+    a = struct()
+    known = {f[0]: f[1] for f in struct._fields_}
+    for k, v in kw.items():
+        if k not in known:
+            raise TypeError(f"{struct.__name__} has no field {k!r}")
+        setattr(a, k, (v or None) if known[k] is ctypes.c_void_p else v)
+    return a
+
+
+def make_kv_cache(**kw) -> ft_kv_cache:
+    return _args(ft_kv_cache, kw)
+
+
+def make_plan_args(**kw) -> ft_plan_args:
+    return _args(ft_plan_args, kw)
+
+
+def make_qk_args(**kw) -> ft_qk_args:
+    return _args(ft_qk_args, kw)
+
+
+def make_attn_args(**kw) -> ft_attn_args:
+    return _args(ft_attn_args, kw)
+
+
+def make_logprob_args(**kw) -> ft_logprob_args:
+    return _args(ft_logprob_args, kw)
+
+
+def ft_kv_plan(args: ft_plan_args, stream: int = 0) -> None:
+    """Block tables, slots, positions and ancestor masks of a step."""
+    _chk(load().ft_kv_plan(args, stream))
+
+
+def ft_qk_norm_rope(args: ft_qk_args, stream: int = 0) -> None:
+    """Per-head norms and rotation of queries and keys; keys and values into the paged cache."""
+    _chk(load().ft_qk_norm_rope(args, stream))
+
+
+def ft_tree_attention_workspace(args: ft_attn_args) -> int:
+    """Bytes of the (once zero-filled) workspace ft_tree_attention needs for these args' sizes."""
+    n = ctypes.c_uint64()
+    _chk(load().ft_tree_attention_workspace(args, ctypes.byref(n)))
+    return n.value
+
+
+def ft_tree_attention(args: ft_attn_args, stream: int = 0) -> None:
+    """Attention of a step's tokens (single, in sequence, or trees) over the paged cache."""
+    _chk(load().ft_tree_attention(args, stream))
+
+
+def ft_token_logprobs(args: ft_logprob_args, stream: int = 0) -> None:
+    """Log probabilities of given tokens, entropy and top alternatives of rows of logits."""
+    _chk(load().ft_token_logprobs(args, stream))
 
 
 class HostPool:

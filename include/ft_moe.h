@@ -75,9 +75,14 @@ extern "C" {
 #define FT_ST_CLOCK_WRAP 4u  /* the LRU step clock reached 2^32 - 1 */
 #define FT_ST_BAD_SLOT 8u    /* a slot id outside [0, S) reached a kernel */
 #define FT_ST_TIMEOUT 16u    /* a bounded wait for an asynchronous copy ran out; the kernel exited early */
+#define FT_ST_NO_ROOM 32u    /* ft_kv_plan: free pages, block-table columns or token rows ran out, or a length was negative */
+#define FT_ST_BAD_TREE 64u   /* a drafted token's parent was not an earlier token of its request, or the tree exceeded mask_words */
+#define FT_ST_BAD_TOKEN 128u /* a token id outside [0, V) or a position outside [0, max_pos) */
 
 #define FT_DTYPE_BF16 0
-#define FT_DTYPE_MXFP4 1
+#define FT_DTYPE_MXFP4 1 /* expert weights only */
+#define FT_DTYPE_F16 2   /* attention-side operators */
+#define FT_DTYPE_F32 3   /* logits of ft_token_logprobs */
 
 #define FT_DECODE_CACHED 0 /* experts from the shared cache, after ft_cache_step */
 #define FT_PREFILL_LAYER 1 /* experts from the full-layer buffers */
@@ -426,6 +431,195 @@ int ft_cpu_executor(ft_ctx* ctx, int threads);
 int ft_cpu_experts(const void* pool_host, int num_experts, int top_k, int hidden, int inter, int dtype, int layer,
                    int T, const int32_t* ids, const float* weights, const int32_t* slot_ids,
                    const uint16_t* hidden_rows, float* partial, int threads);
+
+/* ---- The attention side of a step ----
+ *
+ * Four calls carry a step's tokens around the expert layers over a paged
+ * key/value cache.  A step gives each of num_reqs requests a number of new
+ * tokens: one (decode), several in sequence, or a tree of drafted tokens.  The
+ * new tokens of all requests lie one request after another in rows
+ * q_start[b] .. q_start[b+1]-1 ("row" below).  All four take no context, keep
+ * no state between calls, enqueue on `stream`, never synchronise and can be
+ * captured in a CUDA graph: lengths live on the device, the host gives
+ * capacities.  Host-side faults return FT_E_ARG (a value no step can have) or
+ * FT_E_UNSUPPORTED (one that no kernel is built for); device-side faults set
+ * bits in *status (a device uint32 the caller zeroes, or NULL) and the
+ * offending row, key or page counts as absent.  A call with no rows (T,
+ * max_tokens or num_reqs 0) is FT_OK and does nothing (ft_kv_plan with num_reqs
+ * 0 still marks its rows as padding). */
+
+/* One layer's paged key/value cache.  Key row r of page p and head h starts at
+ * k + p*k_page_stride + r*k_token_stride + h*k_head_stride (in elements);
+ * head_dim numbers are contiguous.  Slot s is row s % page_size of page
+ * s / page_size.  Any order of the dimensions is allowed, and keys and values
+ * may share one buffer; the base and every stride must be a multiple of 16
+ * bytes. */
+typedef struct ft_kv_cache {
+  void* k;
+  void* v;
+  int32_t dtype;     /* FT_DTYPE_BF16 or FT_DTYPE_F16 */
+  int32_t num_pages; /* >= 1 */
+  int32_t page_size; /* rows of a page: a power of two, 8 .. 4096 */
+  int32_t kv_heads;
+  int32_t head_dim;  /* 64 or 128 (ft_qk_norm_rope: also 256) */
+  int32_t reserved;  /* must be zero */
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+} ft_kv_cache;
+
+/* Block tables, slots, positions and ancestor masks of a step, from the
+ * requests' lengths.  Request b has ctx_len[b] cached tokens in its first
+ * ceil(ctx_len/page_size) pages and gets new_len[b] more.
+ *   q_start      [num_reqs+1] exclusive sums of new_len (at most max_tokens)
+ *   block_table  [num_reqs, table_width]: the pages the new tokens begin are
+ *                taken from the top of the stack free_pages[0 .. *free_count)
+ *                in the order of requests and pages, and written to their
+ *                columns; other entries stay
+ *   *free_left   *free_count less the pages taken
+ *   slots        [max_tokens] cache slot of each row (cached index ctx_len+i
+ *                for row i of the request); -1 for padding rows
+ *   positions    [max_tokens] without parents ctx_len+i, with parents ctx_len
+ *                plus the token's depth in the tree (roots: 0); 0 for padding
+ *   mask         [max_tokens, mask_words] (only with parents): bit j of row i
+ *                (bit j%32 of word j/32) is set if token j of the request is
+ *                an ancestor of token i or i itself; 0 for padding
+ * parents [max_tokens]: the request-local index of each row's parent, -1 for a
+ * child of the context, always less than the row's own index; NULL where new
+ * tokens follow one another.  free_left must not be free_count.  Where pages
+ * or columns run out, slots (and the table's columns) become -1, where rows
+ * run out the last requests' new tokens are cut, and *status gets
+ * FT_ST_NO_ROOM.
+ * Integer results, each equal to the sequential definition. */
+typedef struct ft_plan_args {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  const int32_t* parents;
+  const int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* block_table;
+  int32_t* q_start;
+  int64_t* slots;
+  int32_t* positions;
+  uint32_t* mask;
+  int32_t* free_left;
+  uint32_t* status;
+  int32_t num_reqs;
+  int32_t page_size; /* a power of two */
+  int32_t table_width;
+  int32_t max_tokens;
+  int32_t mask_words; /* 0 without parents */
+  int32_t reserved;   /* must be zero */
+} ft_plan_args;
+int ft_kv_plan(const ft_plan_args* args, void* stream);
+
+/* Norms and rotation of a step's queries and keys, and their way into the
+ * cache, in one pass: for every row t and head
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (q_weight or k_weight, [head_dim])
+ * then the first rot_dim numbers are turned by the angles of positions[t]:
+ * with c, s = cos_sin[position][0 .. rot_dim/2), [rot_dim/2 .. rot_dim),
+ *   (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i),
+ * a, b = i, i + rot_dim/2, or 2i, 2i+1 where interleaved != 0.  Queries go to
+ * q_out, keys to cache.k at slots[t], values unchanged to cache.v.  All in 32
+ * bits, rounded once.  Heads are contiguous in a row, rows `*_stride` elements
+ * apart (any stride; 16-byte multiples run faster).  q_out may be q (same
+ * stride).  A negative slot writes no key and value; a slot past the cache is
+ * reported (FT_ST_BAD_SLOT) and writes none; a position outside [0, max_pos)
+ * is reported (FT_ST_BAD_TOKEN), its keys and values are not written and its
+ * queries are zero.  Two rows must not share a slot.
+ * rot_dim: a multiple of 16, 0 .. head_dim.  head_dim: 64, 128 or 256. */
+typedef struct ft_qk_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin; /* [max_pos, rot_dim] */
+  const int32_t* positions;
+  const int64_t* slots;
+  void* q_out;
+  uint32_t* status;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int32_t T;
+  int32_t q_heads;
+  int32_t rot_dim;
+  int32_t max_pos;
+  int32_t interleaved;
+  float eps;
+  ft_kv_cache cache; /* its dtype is that of q, k, v, the weights and q_out */
+} ft_qk_args;
+int ft_qk_norm_rope(const ft_qk_args* args, void* stream);
+
+/* Attention of a step's tokens over the paged cache (the new tokens' own keys
+ * and values already in it).  Request b's keys are cached tokens 0 ..
+ * ctx_len[b] + n - 1, n = q_start[b+1] - q_start[b]; row i of the request sees
+ * the ctx_len[b] keys of the context and new key j where bit j of its mask is
+ * set (mask == NULL: where j <= i).  q_heads is a multiple of cache.kv_heads;
+ * query head h reads key head h / (q_heads / kv_heads).
+ *   out[t, h] = sum_j p_j v_j,  p = softmax over the seen keys of scale * q.k_j
+ *   lse[t, h] = ln sum_j exp(scale * q.k_j)        (float32, may be NULL)
+ * A row that sees no key gives 0 and -inf.  Keys a row does not see take no
+ * part, whatever their bits; cache rows past a request's keys are never used.
+ * Rows at or past q_start[num_reqs] are not written.  Scores, the softmax's
+ * maximum and sum and the output's sum are held in 32 bits; the
+ * probabilities are rounded to the cache's type for the second product.
+ * q and out: [max_tokens, q_heads, head_dim] with rows q_stride / out_stride
+ * elements apart (multiples of 16 bytes), in the cache's type.
+ * workspace: ft_tree_attention_workspace bytes, 16-byte aligned, zero-filled
+ * once by the caller before its first use; every call leaves it ready for
+ * the next.  Calls that may overlap on the GPU need one each. */
+typedef struct ft_attn_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* q_start;     /* [num_reqs + 1] */
+  const int32_t* ctx_len;     /* [num_reqs] */
+  const int32_t* block_table; /* [num_reqs, table_width] */
+  const uint32_t* mask;       /* [max_tokens, mask_words] or NULL */
+  void* workspace;
+  uint32_t* status;
+  int64_t q_stride, out_stride;
+  uint64_t workspace_bytes;
+  int32_t max_tokens;
+  int32_t num_reqs;
+  int32_t q_heads;
+  int32_t table_width;
+  int32_t mask_words; /* new tokens of a request past 32*mask_words are seen by none; 0 without mask */
+  float scale;
+  ft_kv_cache cache;
+} ft_attn_args;
+int ft_tree_attention(const ft_attn_args* args, void* stream);
+
+/* Workspace bytes for ft_tree_attention with these args' max_tokens, num_reqs,
+ * q_heads and cache (pointers are not looked at). */
+int ft_tree_attention_workspace(const ft_attn_args* args, uint64_t* bytes);
+
+/* Scores of T rows of logits [T, V] (row_stride elements apart, any alignment
+ * of the type): with p = softmax(row),
+ *   logprob[t]  = ln p[tokens[t]]              (tokens and logprob may be NULL)
+ *   entropy[t]  = -sum p ln p                  (may be NULL)
+ *   top_ids, top_logprobs [T, top_n]: the top_n largest logits' ids and ln p,
+ *     in descending order, ties to the lower id (top_n 0 .. 32, <= V).
+ * One pass over the logits, sums in 32 bits.  -inf logits are entries of
+ * probability 0; a NaN logit is reported (FT_ST_NAN) and counts as -inf.  A
+ * row of nothing but such has logprob and top_logprobs -inf and entropy 0.  A
+ * row with a +inf logit is reported (FT_ST_NAN): its logprobs and entropy are
+ * NaN.  A token id outside [0, V) is reported (FT_ST_BAD_TOKEN) and its
+ * logprob is NaN; one that is negative is padding: NaN, not reported. */
+typedef struct ft_logprob_args {
+  const void* logits;
+  const int32_t* tokens;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  uint32_t* status;
+  int64_t row_stride;
+  int32_t dtype; /* FT_DTYPE_BF16, FT_DTYPE_F16 or FT_DTYPE_F32 */
+  int32_t T;
+  int32_t V;
+  int32_t top_n;
+} ft_logprob_args;
+int ft_token_logprobs(const ft_logprob_args* args, void* stream);
 
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);

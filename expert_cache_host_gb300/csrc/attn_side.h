@@ -55,6 +55,9 @@ inline int check_kv_cache(const ft_kv_cache& c, bool head_256) {
   for (int64_t x : s)
     if (x < 0 || x % 8 || x >= (int64_t(1) << 38))
       return record_error(FT_E_ARG, "cache strides must be non-negative multiples of 8 elements below 2^38");
+  if (!c.k_token_stride || !c.v_token_stride || (c.kv_heads > 1 && (!c.k_head_stride || !c.v_head_stride)) ||
+      (c.num_pages > 1 && (!c.k_page_stride || !c.v_page_stride)))
+    return record_error(FT_E_ARG, "the cache's rows, heads and pages must not share memory (a stride is 0)");
   if (!is_16b(c.k) || !is_16b(c.v)) return record_error(FT_E_ARG, "the cache must be 16-byte aligned");
   return FT_OK;
 }

@@ -75,7 +75,8 @@ BAD_CACHE = [(dict(k=0), ft.FT_E_ARG), (dict(v=0), ft.FT_E_ARG), (dict(dtype=ft.
              (dict(page_size=24), ft.FT_E_UNSUPPORTED), (dict(page_size=8192), ft.FT_E_UNSUPPORTED),
              (dict(head_dim=96), ft.FT_E_UNSUPPORTED), (dict(k=PTR + 2), ft.FT_E_ARG), (dict(v=PTR + 8), ft.FT_E_ARG),
              (dict(k_token_stride=130), ft.FT_E_ARG), (dict(v_page_stride=-8), ft.FT_E_ARG),
-             (dict(v_head_stride=1 << 38), ft.FT_E_ARG), (dict(reserved=1), ft.FT_E_ARG)]
+             (dict(v_head_stride=1 << 38), ft.FT_E_ARG), (dict(k_token_stride=0), ft.FT_E_ARG),
+             (dict(k_head_stride=0), ft.FT_E_ARG), (dict(v_page_stride=0), ft.FT_E_ARG), (dict(reserved=1), ft.FT_E_ARG)]
 
 
 @pytest.mark.parametrize("kw,code", BAD_CACHE, ids=str)

@@ -406,7 +406,7 @@ def ft_qk_norm_rope(args: ft_qk_args, stream: int = 0) -> None:
 
 
 def ft_tree_attention_workspace(args: ft_attn_args) -> int:
-    """Bytes of the (once zero-filled) workspace ft_tree_attention needs for these args' sizes."""
+    """Bytes of the workspace ft_tree_attention needs for these args' sizes."""
     n = ctypes.c_uint64()
     _chk(load().ft_tree_attention_workspace(args, ctypes.byref(n)))
     return n.value

@@ -15,8 +15,8 @@
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same
 //    number of key tiles of the flattened list of items, whatever the lengths;
-//    an item cut over several CTAs leaves partial outputs in the workspace and
-//    the last CTA to finish joins them in order.
+//    an item cut over several CTAs leaves partial outputs in the workspace,
+//    which a second small kernel joins in order.
 //  - two streams of (S, softmax, O) per CTA: while the four softmax warps of
 //    one work, the tensor cores run the other's products.  With more than 128
 //    rows the streams are the two row tiles and share every K and V tile; with
@@ -25,15 +25,19 @@
 //    page (or per half of a head's 128 numbers), running ahead across items.
 //
 // Warps 0-3 and 4-7: softmax of stream 0 and 1 (a thread per row); warp 8: TMA;
-// warp 9: tensor-core issue.  All waits are bounded (FT_ST_TIMEOUT).
+// warp 9: tensor-core issue; warp 10: V rows (below).  All waits
+// are bounded (FT_ST_TIMEOUT).
 //
 // Keys a row does not see get S = -inf by selection, so their bits do not
 // matter.  For V the product would turn 0 x NaN into NaN: rows of V past the
 // request's keys, of absent pages, and non-finite numbers of new tokens are
-// replaced by zero in shared memory before the product (only tiles that can
-// hold such rows are looked at); a row that does see a non-finite new value
-// adds it in the epilogue.
+// replaced by zero in shared memory before the product; a row that does see a
+// non-finite new value adds it in the epilogue.  Only tiles that can hold such
+// rows go through warp 10: their V lands on the stage's `raw` barrier, and the
+// warp passes it on to `full`.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "attn_side.h"
 #include "tcgen05.h"
@@ -44,11 +48,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int KT = 128;        // keys of a tile
-constexpr int kThreads = 384;  // 8 softmax warps, TMA, issue, two that only fill their warpgroup
+constexpr int kThreads = 384;  // 8 softmax warps, TMA, issue, V fixer, one that only fills its warpgroup
 // Registers a thread: 168 at launch; the softmax warpgroups hold a row of S (128) and take the third's.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the split must fit the launch's registers");
-constexpr int kProducer = 8, kIssuer = 9;  // warps
+constexpr int kProducer = 8, kIssuer = 9, kFixer = 10;  // warps
 // The running maximum may lag behind by this much (in log2 units) before O is
 // rescaled: p <= 2^8 stays exact in fp32 sums and in range of f16.
 constexpr float kLag = 8.f;
@@ -69,10 +73,15 @@ struct Args {
   bool neg;               // scale < 0
   float* part_o;          // [2 grid][256][D]
   float* part_lse;        // [2 grid][256], log2 units
-  unsigned int* count;    // [grid] parts done of the item that begins to be cut at this CTA
+  struct Cut* cut;        // [grid] the item that begins at this CTA and goes on at the next
 };
 
-__host__ __device__ constexpr size_t count_bytes(int grid) { return ((size_t)grid * 4 + 255) / 256 * 256; }
+// An item cut over several CTAs: parts = 0 where there is none.
+struct Cut {
+  int parts, rows, token0, h, pad[4];
+};
+
+__host__ __device__ constexpr size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256; }
 __host__ __device__ constexpr size_t lse_bytes(int grid) { return (size_t)grid * 2 * 256 * 4; }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -80,6 +89,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -103,16 +118,14 @@ __device__ __forceinline__ long long units(const Args& g, int b) {
 }
 
 struct Walk {
-  long long at, end, total;  // in tiles of the flattened list
-  int grid;                  // CTAs that share it
-  int b, h, blk, tile;       // the next tile
+  int left;             // tiles of this CTA's share still to come
+  int b, h, blk, tile;  // the next tile
   Req r;
   // the current item
-  int t0, t1;                // its tiles [t0, t1) are this CTA's
-  int rows;                  // valid rows of the block (tokens * G)
-  bool pair;                 // two row tiles
+  int t0, t1;  // its tiles [t0, t1) are this CTA's
+  bool pair;   // two row tiles
   __device__ __forceinline__ bool next(const Args& g) {
-    if (at >= end) return false;
+    if (left <= 0) return false;
     while (tile >= r.tiles || r.n == 0) {
       tile = 0;
       if (r.n == 0 || ++blk >= r.blocks) {
@@ -124,12 +137,10 @@ struct Walk {
       }
     }
     t0 = tile;
-    t1 = (int)min((long long)r.tiles, tile + (end - at));
-    at += t1 - t0;
+    t1 = min(r.tiles, tile + left);
+    left -= t1 - t0;
     tile = t1;
-    const int tok = min(r.n - blk * 2 * g.tpt, 2 * g.tpt);
-    rows = tok * g.G;
-    pair = tok > g.tpt;
+    pair = r.n - blk * 2 * g.tpt > g.tpt;
     return true;
   }
   // key tiles of a stream, and a stream's j-th
@@ -137,18 +148,24 @@ struct Walk {
   __device__ __forceinline__ int tile_of(int s, int j) const { return pair ? t0 + j : t0 + 2 * j + s; }
 };
 
+// Quotient of non-negative numbers, in 32 bits where they fit (a 64-bit
+// division is a long chain at the head of every CTA).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 struct Shared {
   uint64_t full[12], empty[12];
+  uint64_t raw[12];        // the stage's V has landed but is not fit for the product yet
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2];
   uint32_t tmem;
   uint32_t pages[12];      // per stage: which pages of the tile are there
   uint32_t s_pages[2];     // of the K tile behind a stream's S
-  uint32_t nonfinite[2];   // per item parity: a new token's values held inf or NaN
+  uint32_t nonfinite[4];   // per item (mod 4): a new token's values held inf or NaN
   long long red[kThreads / 32];
-  long long at, total;     // start of this CTA's share: units into request b
+  long long at;            // start of this CTA's share: units into request b
   int b;
-  int last;                // this CTA joins the parts
   float lse[2][128], inv[2][128];  // a row's streams: log2 sum with its maximum, 1 / sum
 };
 
@@ -184,10 +201,50 @@ __device__ __forceinline__ uint32_t visible(const Args& g, const Req& r, const u
   return v;
 }
 
-template <typename E, int D>
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  constexpr uint32_t x = Elem<E>::kDtype == FT_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
-  return (w & x) == x || (w >> 16 & x) == x;
+// Rows of a V tile that must not reach the product: rows [left, last) past the
+// request's keys and rows of absent pages become zero, and so do non-finite
+// numbers in the new tokens' rows [fresh, left); returns whether there were any.
+// One warp.
+template <typename E, int HALVES, int BLOCK>
+__device__ __forceinline__ uint32_t fix_v(uint8_t* v, int lane, int row_shift, uint32_t pages, int left, int last,
+                                          int fresh) {
+  constexpr uint32_t x = Elem<E>::kDtype == FT_DTYPE_BF16 ? 0x7F807F80u : 0x7C007C00u;  // both exponents
+  const int rows = min(left, KT);
+  auto chunk = [&](int row0, int i) {
+    return reinterpret_cast<uint4*>(v + (HALVES == 1 ? 0 : ((i >> 3) & 1) * BLOCK) +
+                                    (row0 + i / (8 * HALVES)) * 128 + (i & 7) * 16);
+  };
+  for (int i = lane; i < (last - rows) * 8 * HALVES; i += 32) *chunk(rows, i) = make_uint4(0, 0, 0, 0);
+  const uint32_t used = (rows + (1 << row_shift) - 1) >> row_shift;
+  if ((pages & ((1u << used) - 1)) != (1u << used) - 1) {
+    for (int i = lane; i < rows * 8 * HALVES; i += 32)
+      if (!(pages >> ((i / (8 * HALVES)) >> row_shift) & 1)) *chunk(0, i) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+  bool hit = false;
+#pragma unroll 4
+  for (int i = lane; i < (rows - fresh) * 8 * HALVES; i += 32) {
+    uint4 u = *chunk(fresh, i);
+    uint32_t* e = reinterpret_cast<uint32_t*>(&u);
+    uint32_t all = 0;  // a half with a zero: that exponent is all ones
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t y = (e[k] & x) ^ x;
+      all |= (y - 0x00010001u) & ~y & 0x80008000u;
+    }
+    if (all) {  // (a borrow can also raise the flag: looked at exactly here)
+      bool bad = false;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if ((e[k] & x & 0xFFFFu) == (x & 0xFFFFu)) e[k] &= 0xFFFF0000u, bad = true;
+        if ((e[k] & x & 0xFFFF0000u) == (x & 0xFFFF0000u)) e[k] &= 0xFFFFu, bad = true;
+      }
+      if (bad) *chunk(fresh, i) = u;
+      hit |= bad;
+    }
+  }
+  proxy_fence_writes();
+  return __any_sync(~0u, hit);
 }
 
 template <typename E, int D>
@@ -201,12 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = sq + 2 * C::TILE;
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::SMEM);
   const ft_attn_args& a = g.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.raw[s], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
@@ -214,32 +272,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.s_full[s], 2);  // the products and the issuer's word on the pages
       mbar_init(&sh.p_full[s], 4);
       mbar_init(&sh.o_full[s], 2);
-      sh.nonfinite[s] = 0;
     }
     mbar_init_fence();
   }
   if (warp == kIssuer) tmem_alloc(&sh.tmem, 512);
+  pdl_trigger();  // the join kernel may be set up; it waits for this grid's end
 
   // Total work and where this CTA's share begins.
   Walk wk;
+  long long units_total, lo;  // all tiles; the first of this CTA's share
+  int grid;                   // CTAs that share them
   {
-    long long mine = 0;
-    for (int b = tid; b < a.num_reqs; b += kThreads) mine += units(g, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) sh.red[warp] = mine;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += sh.red[w];
-    wk.total = total;
-    wk.grid = (int)min((long long)gridDim.x, total);
-    const int c = blockIdx.x;
-    wk.at = c < wk.grid ? total * c / wk.grid : 0;
-    wk.end = c < wk.grid ? total * (c + 1) / wk.grid : 0;
-    long long base = 0;
-    for (int b0 = 0; b0 < a.num_reqs && base <= wk.at; b0 += kThreads) {
-      const long long u = b0 + tid < a.num_reqs ? units(g, b0 + tid) : 0;
-      long long x = u;
+    // Inclusive sums of the requests' units over the block, kThreads requests
+    // at a time; with no more requests than that, one pass serves both uses.
+    long long total = 0, u = 0, x = 0;
+    auto scan = [&](int b0) {
+      u = b0 + tid < a.num_reqs ? units(g, b0 + tid) : 0;
+      x = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(~0u, x, o);
@@ -248,15 +297,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncthreads();
       if (lane == 31) sh.red[warp] = x;
       __syncthreads();
-      long long before = base, all = 0;
+      long long all = 0, before = 0;
+#pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += sh.red[w];
-        all += sh.red[w];
+        const long long y = sh.red[w];
+        if (w < warp) before += y;
+        all += y;
       }
-      const long long first = before + x - u;
-      if (wk.at >= first && wk.at < first + u) {
+      x += before;
+      return all;
+    };
+    for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) total += scan(b0);
+    units_total = total;
+    grid = (int)min((long long)gridDim.x, total);
+    const int c = blockIdx.x;
+    lo = c < grid ? quotient(total * c, grid) : 0;
+    wk.left = c < grid ? (int)(quotient(total * (c + 1), grid) - lo) : 0;
+    long long base = 0;
+    for (int b0 = 0; b0 < a.num_reqs && base <= lo; b0 += kThreads) {
+      const long long all = a.num_reqs > kThreads ? scan(b0) : total;
+      const long long first = base + x - u;
+      if (lo >= first && lo < first + u) {
         sh.b = b0 + tid;
-        sh.at = wk.at - first;
+        sh.at = lo - first;
       }
       base += all;
     }
@@ -265,188 +328,187 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     wk.b = sh.b;
     wk.h = wk.blk = wk.tile = 0;
-    if (wk.at < wk.end) {
+    if (wk.left > 0) {
       wk.r = request(g, wk.b);
       const long long per_head = (long long)wk.r.tiles * wk.r.blocks;
-      wk.h = (int)(sh.at / per_head);
+      wk.h = (int)quotient(sh.at, per_head);
       const long long in_head = sh.at - wk.h * per_head;
-      wk.blk = (int)(in_head / wk.r.tiles);
+      wk.blk = (int)quotient(in_head, wk.r.tiles);
       wk.tile = (int)(in_head - (long long)wk.blk * wk.r.tiles);
     }
   }
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = uniform(sh.tmem);
   bool late = false;
 
   if (warp >= kProducer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == kProducer) {
     const int per_tile = g.log2_page >= 7 ? 1 : KT >> g.log2_page;  // pages of a tile
     const int box_rows = KT / per_tile;
-    const uint32_t box_bytes = (uint32_t)box_rows * 128 * C::HALVES;
-    uint32_t it = 0;
-    int item = 0;
-    for (; wk.next(g); ++item) {
-      if (item > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((item - 1) & 1), late)) late = true;
-      const int q_tiles = wk.pair ? 2 : 1;
-      if (lane == 0) {
-        mbar_expect_tx(&sh.q_full, (uint32_t)(q_tiles * g.tpt * g.G * D * 2));
-        for (int s = 0; s < q_tiles; ++s)
-          for (int hf = 0; hf < C::HALVES; ++hf)
-            tensor_g2s_3d(sq + s * C::TILE + hf * C::BLOCK, &map_q, hf * 64, wk.h * g.G,
-                          wk.r.q0 + (wk.blk * 2 + s) * g.tpt, &sh.q_full);
-      }
-      const int32_t* row = a.block_table + (int64_t)wk.b * a.table_width;
-      const int len = wk.r.ctx + wk.r.n;
-      auto page_of = [&](int t) {
-        const long long col = (((long long)t * KT) >> g.log2_page) + lane;
-        return lane < per_tile && t < wk.t1 && col < a.table_width ? row[col] : -1;
-      };
-      int page = page_of(wk.t0);
-      for (int t = wk.t0; t < wk.t1; ++t) {
-        const int next_page = page_of(t + 1);
-        const int key = t * KT + lane * box_rows;  // first key of this lane's page
-        const bool used = lane < per_tile && key < len;
-        const bool there = used && page >= 0 && page < a.cache.num_pages;
-        if (used && !there && a.status) atomicOr(a.status, FT_ST_BAD_SLOT);
-        const uint32_t pages = __ballot_sync(~0u, there);
-        const int y = g.log2_page >= 7 ? (t * KT) & ((1 << g.log2_page) - 1) : 0;
+    const uint32_t full_pages = (1u << per_tile) - 1;
+    // A lane per page of a tile: the page's id, and whether it is there.
+    auto page_of = [&](int t) {
+      const long long col = (((long long)t * KT) >> g.log2_page) + lane;
+      return lane < per_tile && t < wk.t1 && col < a.table_width ? a.block_table[(int64_t)wk.b * a.table_width + col]
+                                                                : -1;
+    };
+    auto used = [&](int t) { return lane < per_tile && t * KT + lane * box_rows < wk.r.ctx + wk.r.n; };
+    auto there = [&](int t, int page) { return used(t) && page >= 0 && page < a.cache.num_pages; };
+    // V tiles that fix_v looks at: new tokens, the end of the request, absent pages
+    auto special = [&](int t, uint32_t pages) { return (t + 1) * KT > wk.r.ctx || pages != full_pages; };
+
+    if (warp == kProducer) {
+      const uint32_t box_bytes = (uint32_t)box_rows * 128 * C::HALVES;
+      uint32_t st = 0, phase = 1;  // the stage to fill and the parity of its last emptying
+      int item = 0;
+      for (; wk.next(g); ++item) {
+        int page = page_of(wk.t0);
+        if (item > 0 && !mbar_wait(&sh.q_empty, (uint32_t)((item - 1) & 1), late)) late = true;
+        const int q_tiles = wk.pair ? 2 : 1;
+        if (lane == 0) {
+          mbar_expect_tx(&sh.q_full, (uint32_t)(q_tiles * g.tpt * g.G * D * 2));
+          for (int s = 0; s < q_tiles; ++s)
+            for (int hf = 0; hf < C::HALVES; ++hf)
+              tensor_g2s_3d(sq + s * C::TILE + hf * C::BLOCK, &map_q, hf * 64, wk.h * g.G,
+                            wk.r.q0 + (wk.blk * 2 + s) * g.tpt, &sh.q_full);
+        }
+        for (int t = wk.t0; t < wk.t1; ++t) {
+          const int next_page = page_of(t + 1);
+          const bool load = there(t, page);
+          if (used(t) && !load && a.status) atomicOr(a.status, FT_ST_BAD_SLOT);
+          const uint32_t pages = __ballot_sync(~0u, load);
+          const int y = g.log2_page >= 7 ? (t * KT) & ((1 << g.log2_page) - 1) : 0;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int st = it % NST;
-          if (it >= NST && !mbar_wait(&sh.empty[st], (uint32_t)(((it / NST) - 1) & 1), late)) late = true;
-          uint8_t* dst = ring + st * C::TILE + lane * box_rows * 128;
-          if (lane == 0) {
-            sh.pages[st] = pages;
-            mbar_expect_tx(&sh.full[st], (uint32_t)__popc(pages) * box_bytes);
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!mbar_wait(&sh.empty[st], phase, late)) late = true;  // the first round passes at once
+            uint64_t* bar = kv && special(t, pages) ? &sh.raw[st] : &sh.full[st];
+            if (lane == 0) {
+              sh.pages[st] = pages;
+              mbar_expect_tx(bar, (uint32_t)__popc(pages) * box_bytes);
+            }
+            __syncwarp();
+            if (load) {
+              uint8_t* dst = ring + st * C::TILE + lane * box_rows * 128;
+#pragma unroll
+              for (int hf = 0; hf < C::HALVES; ++hf)
+                tensor_g2s_4d(dst + hf * C::BLOCK, kv ? &map_v : &map_k, hf * 64, y, wk.h, page, bar);
+            }
+            if (++st == NST) st = 0, phase ^= 1;
+          }
+          page = next_page;
+        }
+      }
+    } else if (warp == kFixer) {
+      uint32_t st = 0, rounds = 0;  // the stage of a tile's V; a bit per stage: parity of its next raw phase
+      for (int item = 0; wk.next(g); ++item) {
+        uint32_t found = 0;
+        for (int t = wk.t0; t < wk.t1; ++t) {
+          if (++st == NST) st = 0;  // past the tile's K
+          const uint32_t pages = __ballot_sync(~0u, there(t, page_of(t)));
+          if (special(t, pages)) {
+            if (!mbar_wait(&sh.raw[st], (rounds >> st) & 1, late)) late = true;
+            rounds ^= 1u << st;
+            const int left = wk.r.ctx + wk.r.n - t * KT;
+            found |= fix_v<E, C::HALVES, C::BLOCK>(ring + st * C::TILE, lane, min(g.log2_page, 7), pages, left,
+                                                   min(KT, (left + 15) & ~15), max(wk.r.ctx - t * KT, 0));
+            if (lane == 0) {
+              sh.nonfinite[item & 3] = found;
+              mbar_arrive_cta(&sh.full[st]);
+            }
+          }
+          if (++st == NST) st = 0;
+        }
+      }
+    } else if (warp == kIssuer) {
+      // The whole warp keeps the loop's state and one elected lane issues: with
+      // warp-uniform numbers the descriptors stay in uniform registers.
+      const bool one = elect_one();
+      constexpr bool BF = Elem<E>::kDtype == FT_DTYPE_BF16;
+      constexpr uint32_t id_qk = umma_idesc_f16(BF, 128, KT, false), id_pv = umma_idesc_f16(BF, 128, D, true);
+      const uint64_t dq0 = umma_desc_sw128(smem_u32(sq));
+      const uint64_t dk0 = umma_desc_sw128(smem_u32(ring)), dv0 = umma_desc_sw128_mn(smem_u32(ring), C::BLOCK);
+      uint32_t base = 0;             // ring position of the item's first stage
+      uint32_t done0 = 0, done1 = 0;  // tiles of each stream so far (barrier phases)
+      for (int item = 0; wk.next(g); ++item) {
+        const bool pair = uniform(wk.pair);
+        const int n_tiles = uniform(wk.t1 - wk.t0), c0 = uniform(wk.count(0)), c1 = uniform(wk.count(1));
+        // 16-key steps of the item's last tile: past the request's keys nothing is multiplied
+        const int last_steps = uniform(
+            wk.t1 == wk.r.tiles ? (min(KT, wk.r.ctx + wk.r.n - (wk.t1 - 1) * KT) + 15) >> 4 : KT / 16);
+        if (!mbar_wait(&sh.q_full, (uint32_t)(item & 1), late)) late = true;
+        auto qk = [&](auto stream, int j) {
+          constexpr int s = decltype(stream)::value;
+          const uint32_t pos = base + 2 * (pair ? j : 2 * j + s), st = pos % NST;
+          if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
+          tc_fence_after();
+          const uint64_t dq = dq0 + (uint32_t)((pair ? s : 0) * (C::TILE >> 4)), dk = dk0 + st * (C::TILE >> 4);
+          if (one) {
+            sh.s_pages[s] = sh.pages[st];
+            mbar_arrive_cta(&sh.s_full[s]);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::BLOCK + (kk & 3) * 32) >> 4;
+              umma_bf16(tmem + 256 + s * 128, dq + off, dk + off, id_qk, kk ? 1u : 0u);
+            }
+            umma_commit(&sh.s_full[s]);
+            if (!pair || s == 1) umma_commit(&sh.empty[st]);
           }
           __syncwarp();
-          if (there) {
+        };
+        auto pv = [&](auto stream, int j) {
+          constexpr int s = decltype(stream)::value;
+          const int i = pair ? j : 2 * j + s;
+          const uint32_t pos = base + 2 * i + 1, st = pos % NST;
+          if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
+          if (!mbar_wait(&sh.p_full[s], ((s ? done1 : done0) + j) & 1, late)) late = true;
+          tc_fence_after();
+          const uint64_t dv = dv0 + st * (C::TILE >> 4);
+          const int steps = i + 1 == n_tiles ? last_steps : KT / 16;
+          if (one) {
+            if (steps == KT / 16) {
 #pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tensor_g2s_4d(dst + hf * C::BLOCK, kv ? &map_v : &map_k, hf * 64, y, wk.h, page, &sh.full[st]);
-          }
-        }
-        page = next_page;
-      }
-    }
-  } else if (warp == kIssuer) {
-    constexpr bool BF = Elem<E>::kDtype == FT_DTYPE_BF16;
-    constexpr uint32_t id_qk = umma_idesc_f16(BF, 128, KT, false), id_pv = umma_idesc_f16(BF, 128, D, true);
-    uint32_t base = 0;     // ring position of the item's first stage
-    uint32_t done[2] = {};  // tiles of each stream so far (barrier phases)
-    int item = 0;
-    for (; wk.next(g); ++item) {
-      if (lane == 0) sh.nonfinite[item & 1] = 0;
-      if (!mbar_wait(&sh.q_full, (uint32_t)(item & 1), late)) late = true;
-      tc_fence_after();
-      const int cnt[2] = {wk.count(0), wk.count(1)};
-      auto qk = [&](int s, int j) {
-        const uint32_t pos = base + 2 * (wk.tile_of(s, j) - wk.t0);
-        const int st = pos % NST;
-        if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
-        tc_fence_after();
-        if (lane == 0) {
-          sh.s_pages[s] = sh.pages[st];
-          mbar_arrive_cta(&sh.s_full[s]);
-          const uint32_t qa = smem_u32(sq + (wk.pair ? s : 0) * C::TILE), ka = smem_u32(ring + st * C::TILE);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::BLOCK + (kk & 3) * 32;
-            umma_bf16(tmem + 256 + s * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), id_qk, kk ? 1u : 0u);
-          }
-          umma_commit(&sh.s_full[s]);
-          if (!wk.pair || s == 1) umma_commit(&sh.empty[st]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int s, int j) {
-        const int t = wk.tile_of(s, j);
-        const uint32_t pos = base + 2 * (t - wk.t0) + 1;
-        const int st = pos % NST;
-        if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
-        uint8_t* v = ring + st * C::TILE;
-        if (!wk.pair || s == 0) {
-          // rows of V that must not reach the product
-          const uint32_t pages = sh.pages[st];
-          const int per_tile = g.log2_page >= 7 ? 1 : KT >> g.log2_page;
-          const int left = wk.r.ctx + wk.r.n - t * KT;  // keys of the request in this tile
-          const bool whole = left >= KT && pages == (per_tile == 32 ? ~0u : (1u << per_tile) - 1);
-          const int fresh = max(wk.r.ctx - t * KT, 0);  // first row of a new token
-          if (!whole || fresh < KT) {
-            const int row_shift = min(g.log2_page, 7);
-            uint32_t found = 0;
-            for (int x = lane; x < 128 * 8 * C::HALVES; x += 32) {
-              const int row = (x >> 3) & 127, hf = x >> 10;
-              uint4* p = reinterpret_cast<uint4*>(v + hf * C::BLOCK + row * 128 + (x & 7) * 16);
-              if (row >= left || !(pages >> (row >> row_shift) & 1)) {
-                *p = make_uint4(0, 0, 0, 0);
-              } else if (row >= fresh) {
-                uint4 u = *p;
-                uint32_t* e = reinterpret_cast<uint32_t*>(&u);
-                bool hit = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (any_nonfinite<E, D>(e[i])) {
-                    constexpr uint32_t inf = BF ? 0x7F80u : 0x7C00u;
-                    if ((e[i] & inf) == inf) e[i] &= 0xFFFF0000u;
-                    if ((e[i] >> 16 & inf) == inf) e[i] &= 0xFFFFu;
-                    hit = true;
-                  }
-                }
-                if (hit) {
-                  *p = u;
-                  found = 1;
-                }
-              }
+              for (int kk = 0; kk < KT / 16; ++kk)
+                umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, dv + kk * (2048 >> 4), id_pv,
+                            kk ? 1u : (j ? 1u : 0u));
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < steps; ++kk)
+                umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, dv + kk * (2048 >> 4), id_pv, kk + j ? 1u : 0u);
             }
-            proxy_fence_writes();
-            if (__any_sync(~0u, found) && lane == 0) sh.nonfinite[item & 1] = 1;
-            __syncwarp();
+            if (!pair || s == 1) umma_commit(&sh.empty[st]);
+            if (j + 1 == (s ? c1 : c0)) {  // the item's output is complete
+              umma_commit(&sh.o_full[s]);
+              mbar_arrive_cta(&sh.o_full[s]);
+            }
           }
+          __syncwarp();
+        };
+        const std::integral_constant<int, 0> S0;
+        const std::integral_constant<int, 1> S1;
+        qk(S0, 0);
+        if (c1 > 0) qk(S1, 0);
+        if (c0 == 1 && one) umma_commit(&sh.q_empty);  // every product with Q has been issued
+        for (int j = 0; j < c0; ++j) {
+          pv(S0, j);
+          if (j + 1 < c0) qk(S0, j + 1);
+          if (j < c1) pv(S1, j);
+          if (j + 1 < c1) qk(S1, j + 1);
+          if (j + 2 == c0 && one) umma_commit(&sh.q_empty);
         }
-        if (!mbar_wait(&sh.p_full[s], (done[s] + j) & 1, late)) late = true;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t va = smem_u32(v);
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, umma_desc_sw128_mn(va + kk * 2048, C::BLOCK),
-                        id_pv, (j | kk) ? 1u : 0u);
-          if (!wk.pair || s == 1) umma_commit(&sh.empty[st]);
-          if (j + 1 == cnt[s]) {
-            umma_commit(&sh.o_full[s]);
-            mbar_arrive_cta(&sh.o_full[s]);
-          }
-        }
-        __syncwarp();
-      };
-      for (int s = 0; s < 2; ++s)
-        if (cnt[s] > 0) qk(s, 0);
-      bool q_done = false;
-      for (int j = 0; j < cnt[0]; ++j) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (j < cnt[s]) {
-            pv(s, j);
-            if (j + 1 < cnt[s]) qk(s, j + 1);
-          }
-        }
-        if (!q_done && j + 2 >= cnt[0]) {  // every product with Q has been issued
-          q_done = true;
-          if (lane == 0) umma_commit(&sh.q_empty);
-        }
+        done0 += c0;
+        done1 += c1;
+        base += 2 * n_tiles;
       }
-      done[0] += cnt[0];
-      done[1] += cnt[1];
-      base += 2 * (wk.t1 - wk.t0);
     }
-  }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 256 + s * 128 + lanes, t_o = tmem + lanes;
+    const uint32_t full_pages = g.log2_page >= 7 ? 1u : (1u << (KT >> g.log2_page)) - 1;
     uint32_t tiles_done = 0, items_of_stream = 0;
+    bool has_cut = false;
+    const int share = wk.left;
     for (int item = 0; wk.next(g); ++item) {
       const Req& r = wk.r;
       const int first_tok = (wk.blk * 2 + (wk.pair ? s : 0)) * g.tpt;
@@ -471,8 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 128; ++c) x[c] = -x[c];
           }
-          const int per_tile = g.log2_page >= 7 ? 1 : KT >> g.log2_page;
-          if ((t + 1) * KT > r.ctx || pages != (1u << per_tile) - 1) {
+          if ((t + 1) * KT > r.ctx || pages != full_pages) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t vis = valid ? visible(g, r, mrow, i, t * KT + w * 32, w, pages) : 0u;
@@ -524,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items_of_stream;
         tc_fence_after();
       }
-      const bool nonfinite = cnt > 0 && sh.nonfinite[item & 1];
+      const bool nonfinite = wk.t1 * KT > r.ctx && sh.nonfinite[item & 3];  // (written where an item has new keys)
       // Rows' output: with a row tile per stream the thread's own; else the two
       // streams' halves of the keys joined, each warpgroup half of the columns.
       float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + log2f(l) : -CUDART_INF_F;
@@ -618,70 +679,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (a.lse)
           a.lse[(int64_t)(r.q0 + i) * a.q_heads + h0] = lse * kLn2;
       }
-      tc_fence_before();
-      if (!whole) {
-        // The CTAs that share the item: the one with its first tile counts.
-        const long long start = wk.at - wk.t1, G64 = wk.grid;  // the item's first unit
-        const int ca = (int)(((start + 1) * G64 - 1) / wk.total), cb = (int)(((start + r.tiles) * G64 - 1) / wk.total);
-        __threadfence();
-        bar_sync(1, 256);
+      if (!whole && wk.t0 == 0) {
+        has_cut = true;
         if (tid == 0) {
-          const unsigned before = atomicAdd(&g.count[ca], 1u);
-          sh.last = before == (unsigned)(cb - ca);
-          if (sh.last) g.count[ca] = 0;
-          __threadfence();
-        }
-        bar_sync(1, 256);
-        if (sh.last) {
-          constexpr int LPR = D / 4;  // lanes per row
-          const int col = (tid % LPR) * 4;
-          const int tile_rows = g.tpt * g.G;
-          for (int x = tid / LPR; x < wk.rows; x += 256 / LPR) {
-            const int tile_s = x >= tile_rows ? 1 : 0, rr = x - tile_s * tile_rows;
-            const int prow = tile_s * 128 + rr;
-            float top = -CUDART_INF_F;
-            bool nan = false;
-            for (int c = ca; c <= cb; ++c) {
-              const float v = __ldcg(&g.part_lse[(c * 2 + (c == ca ? 1 : 0)) * 256 + prow]);
-              nan |= v != v;
-              top = fmaxf(top, v);
-            }
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
-            if (nan) top = CUDART_NAN_F;
-            if (top != -CUDART_INF_F) {
-#pragma unroll 4
-              for (int c = ca; c <= cb; ++c) {
-                const int pr = (c * 2 + (c == ca ? 1 : 0)) * 256 + prow;
-                const float e = ex2(__ldcg(&g.part_lse[pr]) - top);
-                const float4 o = __ldcg(reinterpret_cast<const float4*>(g.part_o + (int64_t)pr * D + col));
-                if (e != 0.f) {
-                  sum += e;
-                  acc.x = fmaf(e, o.x, acc.x), acc.y = fmaf(e, o.y, acc.y);
-                  acc.z = fmaf(e, o.z, acc.z), acc.w = fmaf(e, o.w, acc.w);
-                }
-              }
-            }
-            const float iv = top == -CUDART_INF_F ? 0.f : 1.f / sum;
-            const int ti = wk.blk * 2 * g.tpt + tile_s * g.tpt + rr / g.G, hh = wk.h * g.G + rr % g.G;
-            uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + ti) * a.out_stride +
-                                                  (int64_t)hh * D + col);
-            *dst = make_uint2(Elem<E>::pack(acc.x * iv, acc.y * iv), Elem<E>::pack(acc.z * iv, acc.w * iv));
-            if (a.lse && col == 0)
-              a.lse[(int64_t)(r.q0 + ti) * a.q_heads + hh] =
-                  top == -CUDART_INF_F ? top : (top + log2f(sum)) * kLn2;
-          }
+          // The item's last tile belongs to the CTA c with lo(c) <= it < lo(c+1), lo(c) = total c / grid:
+          // c = ((it + 1) grid - 1) / total.
+          const long long it = lo + (share - wk.left) - wk.t1 + r.tiles - 1;
+          const int cb = (int)quotient((it + 1) * grid - 1, units_total);
+          const int rows = min(r.n - wk.blk * 2 * g.tpt, 2 * g.tpt) * g.G;
+          g.cut[blockIdx.x] = Cut{cb - (int)blockIdx.x + 1, rows, r.q0 + wk.blk * 2 * g.tpt, wk.h};
         }
       }
-      // both warpgroups have read O (and the joined rows' numbers) before either goes on
+      tc_fence_before();
+      // both warpgroups have read O before either goes on
       bar_sync(1, 256);
     }
+    if (tid == 0 && !has_cut) g.cut[blockIdx.x].parts = 0;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kIssuer) tmem_dealloc(tmem, 512);
   if (late && a.status) atomicOr(a.status, FT_ST_TIMEOUT);
+}
+
+// Joins the parts of the items that were cut: a warp per row, block (first
+// CTA of the item, group of rows).  With L_c a part's log2 sum and O_c its
+// normalised output, out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c, parts in the
+// order of their keys.  The parts are in L2.  Launched as a programmatic
+// dependent of the kernel above, so only its last wait is on the critical path.
+constexpr int kJoinRows = 8;
+template <typename E, int D>
+__global__ void __launch_bounds__(kJoinRows * 32) tree_attention_join_kernel(const __grid_constant__ Args g) {
+  pdl_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, x = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int parts = g.cut[c0].parts, rows = g.cut[c0].rows;
+  if (parts == 0 || x >= rows) return;
+  const ft_attn_args& a = g.a;
+  const int tile_rows = g.tpt * g.G, tile = x >= tile_rows ? 1 : 0, rr = x - tile * tile_rows;
+  const int prow = tile * 128 + rr;
+  auto part_row = [&](int p) { return ((c0 + p) * 2 + (p == 0 ? 1 : 0)) * 256 + prow; };
+  // the row's L: lanes over the parts
+  float top = -CUDART_INF_F;
+  bool nan = false;
+  for (int p = lane; p < parts; p += 32) {
+    const float v = g.part_lse[part_row(p)];
+    nan |= v != v;
+    top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (__any_sync(~0u, nan)) top = CUDART_NAN_F;
+  float acc[D / 32] = {}, sum = 0.f;
+  if (top != -CUDART_INF_F) {
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
+      const int pr = part_row(p);
+      const float e = ex2(g.part_lse[pr] - top);
+      const float* o = g.part_o + (int64_t)pr * D + lane * (D / 32);
+      float v[D / 32];
+      if constexpr (D == 128)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+      sum += e;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        if (e != 0.f) acc[k] = fmaf(e, v[k], acc[k]);
+    }
+  }
+  const float inv = top == -CUDART_INF_F ? 0.f : 1.f / sum;
+  const int h = g.cut[c0].h * g.G + rr % g.G;
+  const int64_t t = g.cut[c0].token0 + tile * g.tpt + rr / g.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D) +
+                  lane * (D / 64);
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) dst[k] = Elem<E>::pack(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if (a.lse && lane == 0) a.lse[t * a.q_heads + h] = top == -CUDART_INF_F ? top : (top + log2f(sum)) * kLn2;
 }
 
 int check(const ft_attn_args& a) {
@@ -693,7 +767,7 @@ int check(const ft_attn_args& a) {
   return FT_OK;
 }
 
-uint64_t workspace(int grid, int D) { return count_bytes(grid) + lse_bytes(grid) + (uint64_t)grid * 2 * 256 * D * 4; }
+uint64_t workspace(int grid, int D) { return cut_bytes(grid) + lse_bytes(grid) + (uint64_t)grid * 2 * 256 * D * 4; }
 
 bool cache_map(CUtensorMap* map, void* base, const ft_kv_cache& c, int64_t page, int64_t token, int64_t head, char* msg,
                size_t len) {
@@ -730,7 +804,14 @@ int launch(const Args& g, int grid, cudaStream_t st) {
     configured = dev;
   }
   tree_attention_kernel<E, D><<<grid, kThreads, C::SMEM + sizeof(Shared), st>>>(mq, mk, mv, g);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    const int most = 2 * g.tpt * g.G;  // rows of an item
+    pdl_config(cfg, attr, dim3(grid, (most + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0, st);
+    e = cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<E, D>, g);
+  }
   if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return FT_OK;
 }
@@ -776,9 +857,9 @@ extern "C" int ft_tree_attention(const ft_attn_args* args, void* stream) {
   const float c = (g.neg ? -a.scale : a.scale) * kLog2e;
   g.c = c > 1e-30f ? c : 1e-30f;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  g.count = reinterpret_cast<unsigned int*>(ws);
-  g.part_lse = reinterpret_cast<float*>(ws + count_bytes(grid));
-  g.part_o = reinterpret_cast<float*>(ws + count_bytes(grid) + lse_bytes(grid));
+  g.cut = reinterpret_cast<Cut*>(ws);
+  g.part_lse = reinterpret_cast<float*>(ws + cut_bytes(grid));
+  g.part_o = reinterpret_cast<float*>(ws + cut_bytes(grid) + lse_bytes(grid));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.cache.dtype == FT_DTYPE_BF16)
     return D == 128 ? launch<__nv_bfloat16, 128>(g, grid, st) : launch<__nv_bfloat16, 64>(g, grid, st);

@@ -564,9 +564,8 @@ int ft_qk_norm_rope(const ft_qk_args* args, void* stream);
  * probabilities are rounded to the cache's type for the second product.
  * q and out: [max_tokens, q_heads, head_dim] with rows q_stride / out_stride
  * elements apart (multiples of 16 bytes), in the cache's type.
- * workspace: ft_tree_attention_workspace bytes, 16-byte aligned, zero-filled
- * once by the caller before its first use; every call leaves it ready for
- * the next.  Calls that may overlap on the GPU need one each. */
+ * workspace: ft_tree_attention_workspace bytes, 16-byte aligned, any contents;
+ * calls that may overlap on the GPU need one each. */
 typedef struct ft_attn_args {
   const void* q;
   void* out;

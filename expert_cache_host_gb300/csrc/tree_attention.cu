@@ -71,7 +71,7 @@ struct Args {
   int log2_page, G, tpt;  // query heads per key head; tokens per 128-row tile
   float c;                // |scale| log2 e
   bool neg;               // scale < 0
-  float* part_o;          // [2 grid][256][D]
+  float4* part_o;         // [2 grid][2 row tiles][D / 4][128 rows] of 4 outputs: a warp's rows are contiguous
   float* part_lse;        // [2 grid][256], log2 units
   struct Cut* cut;        // [grid] the item that begins at this CTA and goes on at the next
 };
@@ -88,6 +88,37 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 numbers to an instruction, and a maximum of three.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -112,36 +143,50 @@ __device__ __forceinline__ Req request(const Args& g, int b) {
   r.blocks = (r.n + 2 * g.tpt - 1) / (2 * g.tpt);
   return r;
 }
-__device__ __forceinline__ long long units(const Args& g, int b) {
-  const Req r = request(g, b);
-  return (long long)r.tiles * r.blocks * g.a.cache.kv_heads;
+// A tile costs a CTA this many units: with two row tiles the products and both
+// streams' softmax take 3400 cycles, with one 1750 alone and 2800 when all SMs
+// pull on HBM (D = 128, measured).
+constexpr int kPairUnits = 3, kSingleUnits = 2;
+// Units of all but the last block, and of the last, per tile.
+__device__ __forceinline__ int last_weight(const Args& g, const Req& r) {
+  return r.n - (r.blocks - 1) * 2 * g.tpt > g.tpt ? kPairUnits : kSingleUnits;
+}
+__device__ __forceinline__ long long head_units(const Args& g, const Req& r) {
+  return r.blocks ? (long long)r.tiles * (kPairUnits * (r.blocks - 1) + last_weight(g, r)) : 0;
 }
 
 struct Walk {
-  int left;             // tiles of this CTA's share still to come
-  int b, h, blk, tile;  // the next tile
+  int left;               // units of this CTA's share still to come
+  int b, h, blk, unit;    // the next unit: place in its block
   Req r;
   // the current item
-  int t0, t1;  // its tiles [t0, t1) are this CTA's
-  bool pair;   // two row tiles
+  int weight;             // units of its tiles
+  int t0, t1;             // its tiles [t0, t1) are this CTA's: those whose first unit is
+  bool pair;              // two row tiles
   __device__ __forceinline__ bool next(const Args& g) {
-    if (left <= 0) return false;
-    while (tile >= r.tiles || r.n == 0) {
-      tile = 0;
-      if (r.n == 0 || ++blk >= r.blocks) {
-        blk = 0;
-        if (r.n == 0 || ++h >= g.a.cache.kv_heads) {
-          h = 0;
-          r = request(g, ++b);
+    for (;;) {
+      if (left <= 0) return false;
+      pair = r.n - blk * 2 * g.tpt > g.tpt;
+      weight = pair ? kPairUnits : kSingleUnits;
+      const int size = r.tiles * weight;
+      if (r.n > 0 && unit < size) {
+        const int end = min(size, unit + left);
+        t0 = (unit + weight - 1) / weight;
+        t1 = (end + weight - 1) / weight;
+        left -= end - unit;
+        unit = end;
+        if (t1 > t0) return true;
+      } else {
+        unit = 0;
+        if (++blk >= r.blocks) {
+          blk = 0;
+          if (r.n == 0 || ++h >= g.a.cache.kv_heads) {
+            h = 0;
+            r = request(g, ++b);
+          }
         }
       }
     }
-    t0 = tile;
-    t1 = min(r.tiles, tile + left);
-    left -= t1 - t0;
-    tile = t1;
-    pair = r.n - blk * 2 * g.tpt > g.tpt;
-    return true;
   }
   // key tiles of a stream, and a stream's j-th
   __device__ __forceinline__ int count(int s) const { return pair ? t1 - t0 : (t1 - t0 + 1 - s) / 2; }
@@ -164,8 +209,7 @@ struct Shared {
   uint32_t s_pages[2];     // of the K tile behind a stream's S
   uint32_t nonfinite[4];   // per item (mod 4): a new token's values held inf or NaN
   long long red[kThreads / 32];
-  long long at;            // start of this CTA's share: units into request b
-  int b;
+  Walk start;              // where this CTA's share starts
   float lse[2][128], inv[2][128];  // a row's streams: log2 sum with its maximum, 1 / sum
 };
 
@@ -278,16 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kIssuer) tmem_alloc(&sh.tmem, 512);
   pdl_trigger();  // the join kernel may be set up; it waits for this grid's end
 
-  // Total work and where this CTA's share begins.
-  Walk wk;
-  long long units_total, lo;  // all tiles; the first of this CTA's share
-  int grid;                   // CTAs that share them
+  // Total work and where this CTA's share begins: inclusive sums of the
+  // requests' units over the block, kThreads requests at a time; with no more
+  // requests than that, one pass serves both uses.
+  long long total = 0, lo;  // units of all items; the first of this CTA's share
+  int grid;                 // CTAs that share them
   {
-    // Inclusive sums of the requests' units over the block, kThreads requests
-    // at a time; with no more requests than that, one pass serves both uses.
-    long long total = 0, u = 0, x = 0;
+    Req r{};
+    long long u = 0, x = 0;
     auto scan = [&](int b0) {
-      u = b0 + tid < a.num_reqs ? units(g, b0 + tid) : 0;
+      r = Req{};
+      if (b0 + tid < a.num_reqs) r = request(g, b0 + tid);
+      u = head_units(g, r) * a.cache.kv_heads;
       x = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -308,35 +354,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       return all;
     };
     for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) total += scan(b0);
-    units_total = total;
-    grid = (int)min((long long)gridDim.x, total);
+    // A share is never less than a tile's units, so every CTA between an item's
+    // first and last has a tile of it (the join counts on that).
+    grid = (int)max(1ll, min((long long)gridDim.x, quotient(total, kPairUnits)));
     const int c = blockIdx.x;
-    lo = c < grid ? quotient(total * c, grid) : 0;
-    wk.left = c < grid ? (int)(quotient(total * (c + 1), grid) - lo) : 0;
+    lo = c < grid ? quotient(total * c, grid) : total;
+    const int share = c < grid ? (int)(quotient(total * (c + 1), grid) - lo) : 0;
+    if (tid == 0) sh.start.left = 0;
     long long base = 0;
     for (int b0 = 0; b0 < a.num_reqs && base <= lo; b0 += kThreads) {
       const long long all = a.num_reqs > kThreads ? scan(b0) : total;
       const long long first = base + x - u;
-      if (lo >= first && lo < first + u) {
-        sh.b = b0 + tid;
-        sh.at = lo - first;
+      if (b0 == 0) __syncthreads();
+      if (share > 0 && lo >= first && lo < first + u) {
+        const long long at = lo - first, per_head = quotient(u, a.cache.kv_heads);
+        Walk& w = sh.start;
+        w.left = share;
+        w.b = b0 + tid;
+        w.r = r;
+        w.h = (int)quotient(at, per_head);
+        const long long in_head = at - w.h * per_head;
+        w.blk = min((int)quotient(in_head, (long long)r.tiles * kPairUnits), r.blocks - 1);
+        w.unit = (int)(in_head - (long long)w.blk * r.tiles * kPairUnits);
       }
       base += all;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    wk.b = sh.b;
-    wk.h = wk.blk = wk.tile = 0;
-    if (wk.left > 0) {
-      wk.r = request(g, wk.b);
-      const long long per_head = (long long)wk.r.tiles * wk.r.blocks;
-      wk.h = (int)quotient(sh.at, per_head);
-      const long long in_head = sh.at - wk.h * per_head;
-      wk.blk = (int)quotient(in_head, wk.r.tiles);
-      wk.tile = (int)(in_head - (long long)wk.blk * wk.r.tiles);
-    }
   }
+  Walk wk = sh.start;
   const uint32_t tmem = uniform(sh.tmem);
   bool late = false;
 
@@ -544,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int c = 4; c < 124; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+          const float top = max3(max3(mx[0], mx[1], x[124]), max3(mx[2], mx[3], x[125]), fmaxf(x[126], x[127]));
           const bool grow = (top - m) * g.c > kLag || m == -CUDART_INF_F;  // also the first tile with a key
           if (__any_sync(~0u, grow)) {
             const float f = grow ? (top == -CUDART_INF_F ? 1.f : ex2((m - top) * g.c)) : 1.f;
@@ -564,14 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (grow) m = top;
           }
           const float ref = m == -CUDART_INF_F ? 0.f : m * g.c;
-          float sum[4] = {};
+          const uint64_t c2 = pair2(g.c, g.c), ref2 = pair2(-ref, -ref);
+          uint64_t sum[4] = {};
 #pragma unroll
           for (int c = 0; c < 128; c += 2) {
-            const float p0 = ex2(fmaf(x[c], g.c, -ref)), p1 = ex2(fmaf(x[c + 1], g.c, -ref));
-            sum[(c >> 1) & 3] += p0 + p1;
+            const float2 t2 = split2(fma2(pair2(x[c], x[c + 1]), c2, ref2));
+            const float p0 = ex2(t2.x), p1 = ex2(t2.y);
+            sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pair2(p0, p1));
             u[c >> 1] = Elem<E>::pack(p0, p1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 part = split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+          l += part.x + part.y;
           tmem_st32(t_s, u);
           tmem_st32(t_s + 32, u + 32);
           tmem_wait_st();
@@ -666,9 +716,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dst[k] = make_uint4(Elem<E>::pack(y[8 * k], y[8 * k + 1]), Elem<E>::pack(y[8 * k + 2], y[8 * k + 3]),
                                     Elem<E>::pack(y[8 * k + 4], y[8 * k + 5]), Elem<E>::pack(y[8 * k + 6], y[8 * k + 7]));
             } else {
-              float4* dst = reinterpret_cast<float4*>(g.part_o + (int64_t)part_row * D + c);
+              float4* dst = g.part_o + ((int64_t)(slot * 2 + (wk.pair ? s : 0)) * (D / 4) + c / 4) * 128 + row;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+              for (int k = 0; k < 8; ++k) dst[k * 128] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
             }
           }
         }
@@ -682,10 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole && wk.t0 == 0) {
         has_cut = true;
         if (tid == 0) {
-          // The item's last tile belongs to the CTA c with lo(c) <= it < lo(c+1), lo(c) = total c / grid:
+          // The first unit `it` of the item's last tile belongs to the CTA c with lo(c) <= it < lo(c+1),
+          // lo(c) = total c / grid:
           // c = ((it + 1) grid - 1) / total.
-          const long long it = lo + (share - wk.left) - wk.t1 + r.tiles - 1;
-          const int cb = (int)quotient((it + 1) * grid - 1, units_total);
+          const long long it = lo + (share - wk.left) - wk.unit + (long long)(r.tiles - 1) * wk.weight;
+          const int cb = (int)quotient((it + 1) * grid - 1, total);
           const int rows = min(r.n - wk.blk * 2 * g.tpt, 2 * g.tpt) * g.G;
           g.cut[blockIdx.x] = Cut{cb - (int)blockIdx.x + 1, rows, r.q0 + wk.blk * 2 * g.tpt, wk.h};
         }
@@ -703,59 +754,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (late && a.status) atomicOr(a.status, FT_ST_TIMEOUT);
 }
 
-// Joins the parts of the items that were cut: a warp per row, block (first
-// CTA of the item, group of rows).  With L_c a part's log2 sum and O_c its
-// normalised output, out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c, parts in the
-// order of their keys.  The parts are in L2.  Launched as a programmatic
-// dependent of the kernel above, so only its last wait is on the critical path.
-constexpr int kJoinRows = 8;
+// Joins the parts of the items that were cut; the blocks of a column share an
+// item.  With L_c a part's log2 sum and O_c its normalised output,
+// out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c, parts in the order of their
+// keys.  A thread takes 4 outputs of a row.  The parts are in L2.  Launched as
+// a programmatic dependent of the kernel above.
+// (kJoinBatch parts' loads are in flight at a time: the kernel is latency.)
+constexpr int kJoinThreads = 256, kJoinBlocks = 8, kJoinBatch = 8;
 template <typename E, int D>
-__global__ void __launch_bounds__(kJoinRows * 32) tree_attention_join_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kJoinThreads) tree_attention_join_kernel(const __grid_constant__ Args g) {
   pdl_wait();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31, x = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-  const int parts = g.cut[c0].parts, rows = g.cut[c0].rows;
-  if (parts == 0 || x >= rows) return;
+  const int c0 = blockIdx.x;
+  const Cut cut = g.cut[c0];
+  if (cut.parts == 0) return;
   const ft_attn_args& a = g.a;
-  const int tile_rows = g.tpt * g.G, tile = x >= tile_rows ? 1 : 0, rr = x - tile * tile_rows;
-  const int prow = tile * 128 + rr;
-  auto part_row = [&](int p) { return ((c0 + p) * 2 + (p == 0 ? 1 : 0)) * 256 + prow; };
-  // the row's L: lanes over the parts
-  float top = -CUDART_INF_F;
-  bool nan = false;
-  for (int p = lane; p < parts; p += 32) {
-    const float v = g.part_lse[part_row(p)];
-    nan |= v != v;
-    top = fmaxf(top, v);
-  }
+  const int tile_rows = g.tpt * g.G;
+  for (int x = blockIdx.y * kJoinThreads + threadIdx.x; x < cut.rows * (D / 4); x += kJoinBlocks * kJoinThreads) {
+    const int col = x / cut.rows, rr = x - col * cut.rows;  // rows fastest: contiguous in the parts
+    const int tile = rr >= tile_rows ? 1 : 0, row = rr - tile * tile_rows;
+    auto slot = [&](int p) { return (c0 + p) * 2 + (p == 0 ? 1 : 0); };
+    float top = -CUDART_INF_F, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool nan = false;
+    for (int p0 = 0; p0 < cut.parts; p0 += kJoinBatch) {
+      float l[kJoinBatch];
+      float4 o[kJoinBatch];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (__any_sync(~0u, nan)) top = CUDART_NAN_F;
-  float acc[D / 32] = {}, sum = 0.f;
-  if (top != -CUDART_INF_F) {
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p) {
-      const int pr = part_row(p);
-      const float e = ex2(g.part_lse[pr] - top);
-      const float* o = g.part_o + (int64_t)pr * D + lane * (D / 32);
-      float v[D / 32];
-      if constexpr (D == 128)
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-      else
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
-      sum += e;
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const int at = slot(min(p0 + i, cut.parts - 1));
+        l[i] = __ldcg(&g.part_lse[at * 256 + tile * 128 + row]);
+        o[i] = __ldcg(&g.part_o[((int64_t)(at * 2 + tile) * (D / 4) + col) * 128 + row]);
+      }
+      float most = top;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k)
-        if (e != 0.f) acc[k] = fmaf(e, v[k], acc[k]);
+      for (int i = 0; i < kJoinBatch; ++i) {
+        if (p0 + i >= cut.parts) l[i] = -CUDART_INF_F;
+        nan |= l[i] != l[i];
+        most = fmaxf(most, l[i]);
+      }
+      if (most == -CUDART_INF_F) continue;
+      const float f = ex2(top - most);
+      top = most;
+      sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const float e = ex2(l[i] - most);
+        if (e > 0.f) {
+          sum += e;
+          acc.x = fmaf(e, o[i].x, acc.x), acc.y = fmaf(e, o[i].y, acc.y);
+          acc.z = fmaf(e, o[i].z, acc.z), acc.w = fmaf(e, o[i].w, acc.w);
+        }
+      }
     }
+    if (nan) sum = CUDART_NAN_F;  // a part's scores held NaN: the row is NaN
+    const float inv = top == -CUDART_INF_F && !nan ? 0.f : 1.f / sum;
+    const int h = cut.h * g.G + row % g.G;
+    const int64_t t = cut.token0 + tile * g.tpt + row / g.G;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + col * 4) =
+        make_uint2(Elem<E>::pack(acc.x * inv, acc.y * inv), Elem<E>::pack(acc.z * inv, acc.w * inv));
+    if (a.lse && col == 0) a.lse[t * a.q_heads + h] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
   }
-  const float inv = top == -CUDART_INF_F ? 0.f : 1.f / sum;
-  const int h = g.cut[c0].h * g.G + rr % g.G;
-  const int64_t t = g.cut[c0].token0 + tile * g.tpt + rr / g.G;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D) +
-                  lane * (D / 64);
-#pragma unroll
-  for (int k = 0; k < D / 64; ++k) dst[k] = Elem<E>::pack(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if (a.lse && lane == 0) a.lse[t * a.q_heads + h] = top == -CUDART_INF_F ? top : (top + log2f(sum)) * kLn2;
 }
 
 int check(const ft_attn_args& a) {
@@ -808,8 +866,7 @@ int launch(const Args& g, int grid, cudaStream_t st) {
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
-    const int most = 2 * g.tpt * g.G;  // rows of an item
-    pdl_config(cfg, attr, dim3(grid, (most + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0, st);
+    pdl_config(cfg, attr, dim3(grid, kJoinBlocks), dim3(kJoinThreads), 0, st);
     e = cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<E, D>, g);
   }
   if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
@@ -859,7 +916,7 @@ extern "C" int ft_tree_attention(const ft_attn_args* args, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   g.cut = reinterpret_cast<Cut*>(ws);
   g.part_lse = reinterpret_cast<float*>(ws + cut_bytes(grid));
-  g.part_o = reinterpret_cast<float*>(ws + cut_bytes(grid) + lse_bytes(grid));
+  g.part_o = reinterpret_cast<float4*>(ws + cut_bytes(grid) + lse_bytes(grid));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.cache.dtype == FT_DTYPE_BF16)
     return D == 128 ? launch<__nv_bfloat16, 128>(g, grid, st) : launch<__nv_bfloat16, 64>(g, grid, st);

@@ -125,6 +125,9 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
   return p != 0;
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -147,12 +150,15 @@ __device__ __forceinline__ Req request(const Args& g, int b) {
 // streams' softmax take 3400 cycles, with one 1750 alone and 2800 when all SMs
 // pull on HBM (D = 128, measured).
 constexpr int kPairUnits = 3, kSingleUnits = 2;
+// An item costs this much besides (its Q, the first tile's way through the
+// pipeline, its output), counted after its tiles.
+constexpr int kItemUnits = 3;
 // Units of all but the last block, and of the last, per tile.
 __device__ __forceinline__ int last_weight(const Args& g, const Req& r) {
   return r.n - (r.blocks - 1) * 2 * g.tpt > g.tpt ? kPairUnits : kSingleUnits;
 }
 __device__ __forceinline__ long long head_units(const Args& g, const Req& r) {
-  return r.blocks ? (long long)r.tiles * (kPairUnits * (r.blocks - 1) + last_weight(g, r)) : 0;
+  return r.blocks ? (long long)r.tiles * (kPairUnits * (r.blocks - 1) + last_weight(g, r)) + kItemUnits * r.blocks : 0;
 }
 
 struct Walk {
@@ -160,19 +166,17 @@ struct Walk {
   int b, h, blk, unit;    // the next unit: place in its block
   Req r;
   // the current item
-  int weight;             // units of its tiles
   int t0, t1;             // its tiles [t0, t1) are this CTA's: those whose first unit is
   bool pair;              // two row tiles
   __device__ __forceinline__ bool next(const Args& g) {
     for (;;) {
       if (left <= 0) return false;
       pair = r.n - blk * 2 * g.tpt > g.tpt;
-      weight = pair ? kPairUnits : kSingleUnits;
-      const int size = r.tiles * weight;
+      const int size = r.tiles * weight() + kItemUnits;
       if (r.n > 0 && unit < size) {
         const int end = min(size, unit + left);
-        t0 = (unit + weight - 1) / weight;
-        t1 = (end + weight - 1) / weight;
+        t0 = tiles_before(unit);
+        t1 = tiles_before(end);
         left -= end - unit;
         unit = end;
         if (t1 > t0) return true;
@@ -188,22 +192,40 @@ struct Walk {
       }
     }
   }
+  __device__ __forceinline__ int weight() const { return pair ? kPairUnits : kSingleUnits; }
+  // tiles of the block whose first unit lies before `u`
+  __device__ __forceinline__ int tiles_before(int u) const {
+    return min(r.tiles, pair ? (u + kPairUnits - 1) / kPairUnits : (u + kSingleUnits - 1) / kSingleUnits);
+  }
   // key tiles of a stream, and a stream's j-th
   __device__ __forceinline__ int count(int s) const { return pair ? t1 - t0 : (t1 - t0 + 1 - s) / 2; }
   __device__ __forceinline__ int tile_of(int s, int j) const { return pair ? t0 + j : t0 + 2 * j + s; }
 };
 
-// Quotient of non-negative numbers, in 32 bits where they fit (a 64-bit
-// division is a long chain at the head of every CTA).
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
+// Units are dealt to `grid` CTAs in order, `per` each and one more to the first `extra`.
+struct Deal {
+  int per, extra, grid;
+  __device__ __forceinline__ Deal(long long total, int ctas) {
+    // A share is never less than a tile's units, so every CTA between an item's
+    // first and last has a tile of it (the join counts on that).
+    const uint32_t t = (uint32_t)min(total, 0x7FFFFFFFll);  // more than 2^31 units: the last CTA takes what is left
+    grid = max(1, min(ctas, (int)(t / kPairUnits)));
+    per = (int)(t / (uint32_t)grid);
+    extra = (int)(t - (uint32_t)per * grid);
+  }
+  __device__ __forceinline__ long long first(int c) const { return (long long)c * per + min(c, extra); }
+  __device__ __forceinline__ int owner(long long unit) const {
+    const uint32_t u = (uint32_t)min(unit, 0x7FFFFFFFll), wide = (uint32_t)extra * (per + 1);
+    const int c = u < wide ? (int)(u / (uint32_t)(per + 1)) : extra + (int)((u - wide) / (uint32_t)max(per, 1));
+    return min(c, grid - 1);
+  }
+};
 
 struct Shared {
   uint64_t full[12], empty[12];
   uint64_t raw[12];        // the stage's V has landed but is not fit for the product yet
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];  // p_half: P's first 64 keys
   uint32_t tmem;
   uint32_t pages[12];      // per stage: which pages of the tile are there
   uint32_t s_pages[2];     // of the K tile behind a stream's S
@@ -304,29 +326,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const ft_attn_args& a = g.a;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
-  if (tid == 0) {
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 1);
-      mbar_init(&sh.raw[s], 1);
-    }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+  if (warp == kIssuer) tmem_alloc(&sh.tmem, 512);
+  if (warp == kProducer) {
+    if (lane < NST) {
+      mbar_init(&sh.full[lane], 1);
+      mbar_init(&sh.empty[lane], 1);
+      mbar_init(&sh.raw[lane], 1);
+    } else if (lane < NST + 2) {
+      const int s = lane - NST;
       mbar_init(&sh.s_full[s], 2);  // the products and the issuer's word on the pages
+      mbar_init(&sh.p_half[s], 4);
       mbar_init(&sh.p_full[s], 4);
       mbar_init(&sh.o_full[s], 2);
+    } else if (lane == NST + 2) {
+      mbar_init(&sh.q_full, 1);
+      mbar_init(&sh.q_empty, 1);
+      sh.start.left = 0;
     }
     mbar_init_fence();
+    if (lane < 3) prefetch_map(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v);
   }
-  if (warp == kIssuer) tmem_alloc(&sh.tmem, 512);
+  // What follows reads what earlier kernels of the stream wrote.
+  pdl_wait();
   pdl_trigger();  // the join kernel may be set up; it waits for this grid's end
 
   // Total work and where this CTA's share begins: inclusive sums of the
   // requests' units over the block, kThreads requests at a time; with no more
   // requests than that, one pass serves both uses.
   long long total = 0, lo;  // units of all items; the first of this CTA's share
-  int grid;                 // CTAs that share them
+  Deal deal(0, 1);
   {
     Req r{};
     long long u = 0, x = 0;
@@ -354,28 +382,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       return all;
     };
     for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) total += scan(b0);
-    // A share is never less than a tile's units, so every CTA between an item's
-    // first and last has a tile of it (the join counts on that).
-    grid = (int)max(1ll, min((long long)gridDim.x, quotient(total, kPairUnits)));
+    deal = Deal(total, gridDim.x);
     const int c = blockIdx.x;
-    lo = c < grid ? quotient(total * c, grid) : total;
-    const int share = c < grid ? (int)(quotient(total * (c + 1), grid) - lo) : 0;
-    if (tid == 0) sh.start.left = 0;
+    lo = deal.first(c);
+    const int share = c >= deal.grid ? 0 : c == deal.grid - 1 ? (int)min(total - lo, 0x7FFFFFFFll) : deal.per + (c < deal.extra);
     long long base = 0;
     for (int b0 = 0; b0 < a.num_reqs && base <= lo; b0 += kThreads) {
       const long long all = a.num_reqs > kThreads ? scan(b0) : total;
       const long long first = base + x - u;
-      if (b0 == 0) __syncthreads();
       if (share > 0 && lo >= first && lo < first + u) {
-        const long long at = lo - first, per_head = quotient(u, a.cache.kv_heads);
+        // (a request of more than 2^32 units does not occur: 2^31 keys are 2^24 tiles)
+        const uint32_t at = (uint32_t)(lo - first), per_head = (uint32_t)head_units(g, r);
+        const uint32_t per_block = (uint32_t)r.tiles * kPairUnits + kItemUnits;
         Walk& w = sh.start;
         w.left = share;
         w.b = b0 + tid;
         w.r = r;
-        w.h = (int)quotient(at, per_head);
-        const long long in_head = at - w.h * per_head;
-        w.blk = min((int)quotient(in_head, (long long)r.tiles * kPairUnits), r.blocks - 1);
-        w.unit = (int)(in_head - (long long)w.blk * r.tiles * kPairUnits);
+        w.h = (int)(at / per_head);
+        const uint32_t in_head = at - w.h * per_head;
+        w.blk = min((int)(in_head / per_block), r.blocks - 1);
+        w.unit = (int)(in_head - w.blk * per_block);
       }
       base += all;
     }
@@ -485,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto qk = [&](auto stream, int j) {
           constexpr int s = decltype(stream)::value;
           const uint32_t pos = base + 2 * (pair ? j : 2 * j + s), st = pos % NST;
-          if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
+          // (a row tile pair's second stream finds the tile its first has waited for)
+          if ((!pair || s == 0) && !mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
           tc_fence_after();
           const uint64_t dq = dq0 + (uint32_t)((pair ? s : 0) * (C::TILE >> 4)), dk = dk0 + st * (C::TILE >> 4);
           if (one) {
@@ -505,22 +532,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int s = decltype(stream)::value;
           const int i = pair ? j : 2 * j + s;
           const uint32_t pos = base + 2 * i + 1, st = pos % NST;
-          if (!mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
-          if (!mbar_wait(&sh.p_full[s], ((s ? done1 : done0) + j) & 1, late)) late = true;
-          tc_fence_after();
+          if ((!pair || s == 0) && !mbar_wait(&sh.full[st], (pos / NST) & 1, late)) late = true;
+          const uint32_t phase = ((s ? done1 : done0) + j) & 1;
           const uint64_t dv = dv0 + st * (C::TILE >> 4);
           const int steps = i + 1 == n_tiles ? last_steps : KT / 16;
-          if (one) {
-            if (steps == KT / 16) {
+          // P comes in two halves, so that the first half's products run beside
+          // the second half's exponentials.
 #pragma unroll
-              for (int kk = 0; kk < KT / 16; ++kk)
-                umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, dv + kk * (2048 >> 4), id_pv,
-                            kk ? 1u : (j ? 1u : 0u));
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < steps; ++kk)
-                umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, dv + kk * (2048 >> 4), id_pv, kk + j ? 1u : 0u);
+          for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(half ? &sh.p_full[s] : &sh.p_half[s], phase, late)) late = true;
+            tc_fence_after();
+            if (one) {
+#pragma unroll
+              for (int k = 0; k < KT / 32; ++k) {
+                const int kk = half * (KT / 32) + k;
+                if (kk < steps)
+                  umma_f16_ta(tmem + s * 128, tmem + 256 + s * 128 + kk * 8, dv + kk * (2048 >> 4), id_pv,
+                              kk ? 1u : (j ? 1u : 0u));
+              }
             }
+          }
+          if (one) {
             if (!pair || s == 1) umma_commit(&sh.empty[st]);
             if (j + 1 == (s ? c1 : c0)) {  // the item's output is complete
               umma_commit(&sh.o_full[s]);
@@ -553,13 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 256 + s * 128 + lanes, t_o = tmem + lanes;
     const uint32_t full_pages = g.log2_page >= 7 ? 1u : (1u << (KT >> g.log2_page)) - 1;
+    const int tok = row / g.G, head = row - tok * g.G;  // this thread's row in any block
     uint32_t tiles_done = 0, items_of_stream = 0;
     bool has_cut = false;
     const int share = wk.left;
     for (int item = 0; wk.next(g); ++item) {
       const Req& r = wk.r;
       const int first_tok = (wk.blk * 2 + (wk.pair ? s : 0)) * g.tpt;
-      const int tok = row / g.G, i = first_tok + tok;
+      const int i = first_tok + tok;
       const bool valid = tok < g.tpt && i < r.n;
       const bool warp_live = __any_sync(~0u, valid);
       const uint32_t* mrow = a.mask ? a.mask + (int64_t)(r.q0 + (valid ? i : 0)) * a.mask_words : nullptr;
@@ -614,17 +647,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t c2 = pair2(g.c, g.c), ref2 = pair2(-ref, -ref);
           uint64_t sum[4] = {};
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            const float2 t2 = split2(fma2(pair2(x[c], x[c + 1]), c2, ref2));
-            const float p0 = ex2(t2.x), p1 = ex2(t2.y);
-            sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pair2(p0, p1));
-            u[c >> 1] = Elem<E>::pack(p0, p1);
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int c = half * 64; c < half * 64 + 64; c += 2) {
+              const float2 t2 = split2(fma2(pair2(x[c], x[c + 1]), c2, ref2));
+              const float p0 = ex2(t2.x), p1 = ex2(t2.y);
+              sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pair2(p0, p1));
+              u[c >> 1] = Elem<E>::pack(p0, p1);
+            }
+            tmem_st32(t_s + half * 32, u + half * 32);
+            tmem_wait_st();
+            tc_fence_before();
+            if (half == 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cta(&sh.p_half[s]);
+            }
           }
           const float2 part = split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
           l += part.x + part.y;
-          tmem_st32(t_s, u);
-          tmem_st32(t_s + 32, u + 32);
-          tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive_cta(&sh.p_half[s]);
         }
         tc_fence_before();
         __syncwarp();
@@ -655,8 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const float e0 = ex2(l0 - top), e1 = ex2(l1 - top);
           lse = top + log2f(e0 + e1);
-          w0 = e0 / (e0 + e1) * sh.inv[0][row];
-          w1 = e1 / (e0 + e1) * sh.inv[1][row];
+          const float f = __fdividef(1.f, e0 + e1);
+          w0 = e0 * f * sh.inv[0][row];
+          w1 = e1 * f * sh.inv[1][row];
         }
         use0 = l0 != -CUDART_INF_F;
         use1 = l1 != -CUDART_INF_F;
@@ -669,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = wk.t0 == 0 && wk.t1 == r.tiles;
       const int slot = blockIdx.x * 2 + (wk.t0 == 0 ? 1 : 0);
       const int part_row = slot * 256 + (wk.pair ? s * 128 : 0) + row;
-      const int h0 = wk.h * g.G + row % g.G;
+      const int h0 = wk.h * g.G + head;
       if (warp_live) {
 #pragma unroll 1
         for (int c = c0; c < c1; c += 32) {
@@ -732,11 +775,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole && wk.t0 == 0) {
         has_cut = true;
         if (tid == 0) {
-          // The first unit `it` of the item's last tile belongs to the CTA c with lo(c) <= it < lo(c+1),
-          // lo(c) = total c / grid:
-          // c = ((it + 1) grid - 1) / total.
-          const long long it = lo + (share - wk.left) - wk.unit + (long long)(r.tiles - 1) * wk.weight;
-          const int cb = (int)quotient((it + 1) * grid - 1, total);
+          // the CTA that owns the first unit of the item's last tile
+          const long long it = lo + (share - wk.left) - wk.unit + (long long)(r.tiles - 1) * wk.weight();
+          const int cb = deal.owner(it);
           const int rows = min(r.n - wk.blk * 2 * g.tpt, 2 * g.tpt) * g.G;
           g.cut[blockIdx.x] = Cut{cb - (int)blockIdx.x + 1, rows, r.q0 + wk.blk * 2 * g.tpt, wk.h};
         }
@@ -861,11 +902,11 @@ int launch(const Args& g, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention setup failed: %s", cudaGetErrorString(e));
     configured = dev;
   }
-  tree_attention_kernel<E, D><<<grid, kThreads, C::SMEM + sizeof(Shared), st>>>(mq, mk, mv, g);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(cfg, attr, dim3(grid), dim3(kThreads), C::SMEM + sizeof(Shared), st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attention_kernel<E, D>, mq, mk, mv, g);
   if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
     pdl_config(cfg, attr, dim3(grid, kJoinBlocks), dim3(kJoinThreads), 0, st);
     e = cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<E, D>, g);
   }

@@ -1,28 +1,32 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of
 // logits in one pass (ft_token_logprobs).
 //
-// With m a running maximum and t = (x - m) log2(e), a row needs
+// With m a running maximum, M = m log2(e) and t = x log2(e) - M, a row needs
 //   S = sum 2^t,   U = sum t 2^t:
 //   ln sum e^x = m + ln 2 log2 S,   entropy = ln 2 (log2 S - U / S),
-// and when t falls by d for a larger m, U <- (U - d S) 2^-d, S <- S 2^-d.
-// (x - m is formed first: with one fused product the reference m log2(e) would
-// overflow for logits near the type's ends.)  Each thread keeps its own
-// (m, S, U) over a batch of kVecs vectors at a time, so one maximum and one
-// rescaling serve the batch; partial sums join in a fixed order.
+// and when t falls by d for a larger m, U <- (U - d S) 2^-d, S <- S 2^-d.  (M is
+// rounded; t at x = m is that rounding, and the result takes it out again.)
 //
-// Alternatives without a second pass over HBM: order all entries by a 64-bit
-// key (value, then lower id), so that no two are equal.  Each thread keeps
-// only its largest value and the batch it came from.  The top_n-th largest of
-// the threads' best keys is a bound: at least top_n entries reach it, and
-// every entry that does belongs to one of exactly top_n threads (a thread's
-// best is at least any of its entries).  So only those threads' entries are
-// looked at again (from L2), a warp per thread, and merged 32 at a time into a
-// sorted list in registers.  The work does not depend on the values beyond
-// that, and equal logits cost nothing extra.
+// HBM bounds many rows, if a batch of logits costs few instructions: 16-bit
+// logits are clamped and their maximum taken in packed pairs, the rest runs on
+// packed fp32 pairs, so that an element is 1 exponential and 3.5 other
+// instructions.  A batch is kVecs 16-byte vectors a thread: one maximum and
+// one rescaling serve it, and the next batch's loads are in flight meanwhile.
+// A batch that holds NaN, or whose maximum lies near the type's ends, is done
+// again with care.
+//
+// Alternatives without a second pass over HBM: each thread keeps only its
+// largest value.  The top_n-th largest of these is a bound that at least top_n
+// entries reach, and only threads whose largest reaches it hold such entries:
+// a warp looks at each such thread's entries again (from L2) and collects those
+// that reach the bound, a little over top_n where few are equal.  They are
+// ordered by a 64-bit key (value, then lower id).  Where they overflow the list
+// (thousands of equal logits) the warps walk all entries, each merging what
+// beats its own top_n-th.
 //
 // A row goes to a cluster of CTAs, each with a stretch of it, so that a few
-// rows still use many SMs; the CTAs' sums and sorted lists join through
-// distributed shared memory.
+// rows still use many SMs; the CTAs' sums and lists are written to the first
+// one's shared memory.  All orders are fixed, so results repeat bit by bit.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -33,17 +37,40 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
-constexpr int kVecs = 4;  // 16-byte loads of a batch
+constexpr int kVecs = 4;     // 16-byte loads of a batch
+constexpr int kList = 1024;  // entries that reach the bound
+constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kHuge = 1e37f;  // up to here m log2(e) is far from overflow
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Larger value, or the lower id among equals, is the larger key; 0 is below every entry.
@@ -58,13 +85,15 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ uint32_t key_id(uint64_t k) { return 0xFFFFFFFFu - (uint32_t)k; }
 
-__device__ __forceinline__ uint64_t order_step(uint64_t k, int lane, int o, bool larger_first) {
-  const uint64_t other = __shfl_xor_sync(~0u, k, o);
+// Bitonic networks over a warp's lanes, larger first.
+template <typename T>
+__device__ __forceinline__ T order_step(T k, int lane, int o, bool larger_first) {
+  const T other = __shfl_xor_sync(~0u, k, o);
   const bool low = (lane & o) == 0;
   return (low == larger_first) == (k > other) ? k : other;
 }
-// The warp's 32 keys in descending order of lane.
-__device__ __forceinline__ uint64_t warp_sort(uint64_t k, int lane) {
+template <typename T>
+__device__ __forceinline__ T warp_sort(T k, int lane) {
 #pragma unroll
   for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -72,43 +101,88 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t k, int lane) {
   return k;
 }
 // The 32 largest of two descending lists, descending.
-__device__ __forceinline__ uint64_t warp_merge(uint64_t a, uint64_t b, int lane) {
-  const uint64_t r = __shfl_sync(~0u, b, 31 - lane);
-  uint64_t k = a > r ? a : r;
+template <typename T>
+__device__ __forceinline__ T warp_merge(T a, T b, int lane) {
+  const T r = __shfl_sync(~0u, b, 31 - lane);
+  T k = a > r ? a : r;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) k = order_step(k, lane, o, true);
   return k;
+}
+// Lists [0, n) (n a power of two) merged into the first; the whole block calls it.
+template <typename T>
+__device__ __forceinline__ void block_merge(T (*list)[kMaxTop], int n, int w, int lane) {
+#pragma unroll 1
+  for (n >>= 1; n > 0; n >>= 1) {
+    __syncthreads();
+    if (w < n) list[w][lane] = warp_merge(list[w][lane], list[w + n][lane], lane);
+  }
+  __syncthreads();
 }
 
 struct Sums {
   float m, s, u;  // reference, sum of 2^t, sum of t 2^t
 };
+__device__ __forceinline__ bool near(float m) { return fabsf(m) < kHuge; }
+// How far t falls when the reference moves from a to b >= a.
+__device__ __forceinline__ float fall(float a, float b) {
+  const float d = near(a) && near(b) ? __fmul_rn(a, kLog2e) - __fmul_rn(b, kLog2e) : (a - b) * kLog2e;
+  return fmaxf(d, -1e30f);  // (also for -inf - -inf)
+}
+// t of the reference itself: the rounding of M.
+__device__ __forceinline__ float rest(float m) { return near(m) ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.f; }
+__device__ __forceinline__ Sums moved(Sums a, float m) {
+  const float d = fall(a.m, m), e = ex2(d);
+  // d 2^d -> 0 as d -> -inf: a part that vanishes adds nothing
+  return Sums{m, a.s * e, e > 0.f ? fmaf(d, a.s, a.u) * e : 0.f};
+}
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
   const float m = fmaxf(a.m, b.m);
   if (m == -CUDART_INF_F) return a;
-  const float da = fmaxf((a.m - m) * kLog2e, -1e30f), db = fmaxf((b.m - m) * kLog2e, -1e30f);
-  const float ea = ex2(da), eb = ex2(db);
-  Sums r;
-  r.m = m;
-  r.s = a.s * ea + b.s * eb;
-  // d * 2^d -> 0 as d -> -inf: a part that vanishes adds nothing
-  r.u = (ea > 0.f ? (a.u + da * a.s) * ea : 0.f) + (eb > 0.f ? (b.u + db * b.s) * eb : 0.f);
-  return r;
+  const Sums x = moved(a, m), y = moved(b, m);
+  return Sums{m, x.s + y.s, x.u + y.u};
+}
+// One entry with care: any value.
+__device__ __forceinline__ void add_entry(Sums& q, float x) {
+  if (!(x > -CUDART_INF_F)) return;  // -inf adds nothing, NaN counts as -inf
+  if (x > q.m) q = moved(q, x);
+  const float t = near(q.m) ? fmaf(x, kLog2e, -__fmul_rn(q.m, kLog2e)) : (x - q.m) * kLog2e;
+  const float e = ex2(fmaxf(t, -1e30f));
+  q.s += e;
+  if (e > 0.f) q.u = fmaf(t, e, q.u);
 }
 
 template <typename E>
-struct Logit;  // 16 bytes of logits <-> floats, and a maximum that keeps NaN
+struct Logit;  // 16 bytes of logits
 template <>
 struct Logit<float> {
   static constexpr int N = 4;
+  static constexpr float kLow = -1e29f;
   static __device__ __forceinline__ void unpack(uint4 w, float* x) {
     x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
   }
+  // every value at least a little below kLow, NaN kept
+  static __device__ __forceinline__ void unpack_clamped(uint4 w, float* x) {
+    unpack(w, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(x[j]) : "f"(-1e30f));
+  }
+  // maximum of a batch's values that are not NaN
+  static __device__ __forceinline__ float largest(const uint4* v) {
+    float m = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
+                         fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
+    return m;
+  }
   static __device__ __forceinline__ float scalar(const float* p) { return __ldg(p); }
 };
-template <typename E>
+template <typename E, typename E2>
 struct Logit16 {
   static constexpr int N = 8;
+  static __device__ __forceinline__ E2 as2(uint32_t w) { return *reinterpret_cast<E2*>(&w); }
+  static __device__ __forceinline__ uint32_t bits(E2 w) { return *reinterpret_cast<uint32_t*>(&w); }
   static __device__ __forceinline__ void unpack(uint4 w, float* x) {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -117,27 +191,48 @@ struct Logit16 {
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
   }
+  static __device__ __forceinline__ void unpack_clamped(uint4 w, float* x) {
+    const E2 low = as2(Logit<E>::kClamp);
+    unpack(make_uint4(bits(__hmax2_nan(as2(w.x), low)), bits(__hmax2_nan(as2(w.y), low)),
+                      bits(__hmax2_nan(as2(w.z), low)), bits(__hmax2_nan(as2(w.w), low))),
+           x);
+  }
+  static __device__ __forceinline__ float largest(const uint4* v) {
+    E2 m = __hmax2(__hmax2(as2(v[0].x), as2(v[0].y)), __hmax2(as2(v[0].z), as2(v[0].w)));
+#pragma unroll
+    for (int i = 1; i < kVecs; ++i)
+      m = __hmax2(m, __hmax2(__hmax2(as2(v[i].x), as2(v[i].y)), __hmax2(as2(v[i].z), as2(v[i].w))));
+    const float2 f = Elem<E>::unpack(bits(m));
+    const float top = fmaxf(f.x, f.y);
+    return top == top ? top : -CUDART_INF_F;
+  }
 };
 template <>
-struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16> {
+struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16, __nv_bfloat162> {
+  static constexpr uint32_t kClamp = 0xF149F149u;  // about -1e30
+  static constexpr float kLow = -1e29f;
   static __device__ __forceinline__ float scalar(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 };
 template <>
-struct Logit<__half> : Logit16<__half> {
+struct Logit<__half> : Logit16<__half, __half2> {
+  static constexpr uint32_t kClamp = 0xFBFFFBFFu;  // -65504
+  static constexpr float kLow = -6e4f;
   static __device__ __forceinline__ float scalar(const __half* p) { return __half2float(*p); }
 };
 
 struct RowShared {
+  uint64_t keys[kList];
   uint64_t list[kWarps][kMaxTop];
-  uint64_t mine[kMaxTop];  // this CTA's best, descending (read by the cluster's first CTA)
-  int cand[kMaxTop];
+  uint64_t from[kMaxCluster][kMaxTop];  // the first CTA's: each CTA's best, descending
+  Sums from_sums[kMaxCluster];
+  int from_nan[kMaxCluster];
+  float best[kWarps][kMaxTop];
   Sums warp_sums[kWarps];
-  Sums sums;  // this CTA's
-  int nan;
+  int count, nan;
 };
 
 template <typename E, int CS>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const ft_logprob_args a) {
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_logprob_args a) {
   using L = Logit<E>;
   constexpr int N = L::N;
   __shared__ RowShared sh;
@@ -145,6 +240,16 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const ft_logpr
   const int rank = CS == 1 ? 0 : (int)(blockIdx.x % CS);
   const int t = blockIdx.x / CS;
   const E* row = static_cast<const E*>(a.logits) + (int64_t)t * a.row_stride;
+  if (tid == 0) sh.count = sh.nan = 0;
+  if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before remote writes
+
+  // The given token's logit, on its way while the row is read.
+  int token = -1;
+  float token_x = 0.f;
+  if (rank == 0 && tid == 0 && a.tokens) {
+    token = a.tokens[t];
+    if (token >= 0 && token < a.V) token_x = L::scalar(row + token);
+  }
 
   // The row: up to N-1 entries before the first 16-byte boundary, whole
   // 16-byte vectors, the rest.  Vectors [v0, v1) are this CTA's.
@@ -155,50 +260,59 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const ft_logpr
   const int per = ((nvec + CS - 1) / CS + kThreads - 1) / kThreads * kThreads;
   const int v0 = min(rank * per, nvec), v1 = min(v0 + per, nvec);
 
-  if (tid == 0) sh.nan = 0;
   Sums q{-CUDART_INF_F, 0.f, 0.f};
-  float best = -CUDART_INF_F;
-  int best_vec = -1;  // first vector of the batch with this thread's largest value
   bool nan = false;
+  uint4 raw[kVecs];
+  // past the end: the batch's first vector again, left out of the sums
+  auto load = [&](int v) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) raw[i] = __ldg(body + (v + i * kThreads < v1 ? v + i * kThreads : v));
+  };
+  if (v0 + tid < v1) load(v0 + tid);
   for (int v = v0 + tid; v < v1; v += kThreads * kVecs) {
-    uint4 raw[kVecs];
+    uint4 cur[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) cur[i] = raw[i];
+    if (v + kThreads * kVecs < v1) load(v + kThreads * kVecs);
+    const float top = L::largest(cur);
+    if (top > q.m) q = moved(q, top);
+    const uint64_t m2 = pair2(-__fmul_rn(q.m, kLog2e), -__fmul_rn(q.m, kLog2e)), l2 = pair2(kLog2e, kLog2e);
+    uint64_t s2[2] = {}, u2[2] = {};
+    const int left = (v1 - v + kThreads - 1) / kThreads;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int vi = v + i * kThreads;
-      raw[i] = __ldg(body + (vi < v1 ? vi : v));  // past the end: the batch's first vector again, not counted below
-    }
-    float bmax = -CUDART_INF_F;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float x[N];
-      L::unpack(raw[i], x);
-#pragma unroll
-      for (int j = 0; j < N; ++j) bmax = fmaxf(bmax, x[j]);
-    }
-    if (bmax > best || best_vec < 0) best = bmax, best_vec = v;
-    if (bmax > q.m) {
-      const float d = fmaxf((q.m - bmax) * kLog2e, -1e30f), e = ex2(d);
-      q.u = e > 0.f ? (q.u + d * q.s) * e : 0.f;
-      q.s *= e;
-      q.m = bmax;
-    }
-    const float ref = q.m == -CUDART_INF_F ? 0.f : q.m;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      if (v + i * kThreads < v1) {
+      if (i < left) {
         float x[N];
-        L::unpack(raw[i], x);
+        L::unpack_clamped(cur[i], x);
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+          const uint64_t t2 = fma2(pair2(x[j], x[j + 1]), l2, m2);
+          const float2 f = split2(t2);
+          const uint64_t e2 = pair2(ex2(f.x), ex2(f.y));
+          s2[(j >> 1) & 1] = add2(s2[(j >> 1) & 1], e2);
+          u2[(j >> 1) & 1] = fma2(t2, e2, u2[(j >> 1) & 1]);
+        }
+      }
+    }
+    const float2 s = split2(add2(s2[0], s2[1])), u = split2(add2(u2[0], u2[1]));
+    const float bs = s.x + s.y;
+    if (bs == bs && q.m >= L::kLow && q.m < kHuge) {
+      q.s += bs;
+      q.u += u.x + u.y;
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kVecs && i < left; ++i) {
+        float x[N];
+        L::unpack(__ldg(body + v + i * kThreads), x);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           nan |= x[j] != x[j];
-          const float tt = fmaxf((x[j] - ref) * kLog2e, -1000.f);  // -inf and NaN: 2^-1000 = 0
-          const float e = ex2(tt);
-          q.s += e;
-          q.u = fmaf(tt, e, q.u);
+          add_entry(q, x[j]);
         }
       }
     }
   }
+  const float best = v0 + tid < v1 ? q.m : CUDART_NAN_F;  // NaN: this thread has no vector
   // entries outside the vectors: at most N-1 on either side, one thread each
   uint64_t edge = 0;
   if (rank == 0 && tid < 32) {
@@ -209,107 +323,115 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const ft_logpr
       const float x = L::scalar(row + id);
       nan |= x != x;
       edge = make_key(x, id);
-      if (x > -CUDART_INF_F) q = join(q, Sums{x, 1.f, 0.f});
+      add_entry(q, x);
     }
   }
-  // the block's sums, in a fixed order
+  // the block's sums, in a fixed order: to the warp's maximum, then added
+  {
+    float m = q.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_down_sync(~0u, q.m, o);
-    b.s = __shfl_down_sync(~0u, q.s, o);
-    b.u = __shfl_down_sync(~0u, q.u, o);
-    q = join(q, b);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (m != -CUDART_INF_F) q = moved(q, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      q.s += __shfl_xor_sync(~0u, q.s, o);
+      q.u += __shfl_xor_sync(~0u, q.u, o);
+    }
+    if (lane == 0) sh.warp_sums[w] = q;
   }
-  if (lane == 0) sh.warp_sums[w] = q;
-  __syncthreads();
-  if (nan) sh.nan = 1;
-  if (tid == 0) {
-    Sums s = sh.warp_sums[0];
-    for (int i = 1; i < kWarps; ++i) s = join(s, sh.warp_sums[i]);
-    sh.sums = s;
-  }
+  if (__any_sync(~0u, nan) && lane == 0) sh.nan = 1;  // (read after the barriers below)
 
   if (a.top_n > 0) {
-    // this thread's best key: the first place of its largest value
-    uint64_t key = 0;
-    if (best_vec >= 0) {
-      for (int i = kVecs - 1; i >= 0; --i) {
-        const int vi = best_vec + i * kThreads;
-        if (vi < v1) {
-          float x[N];
-          L::unpack(__ldg(body + vi), x);
+    // the bound: the top_n-th largest of the threads' largest (-inf: fewer threads)
+    sh.best[w][lane] = warp_sort(best == best ? best : -CUDART_INF_F, lane);
+    block_merge(sh.best, kWarps, w, lane);
+    const float bound = sh.best[0][a.top_n - 1];
+    // the entries that reach it
+    unsigned todo = __ballot_sync(~0u, best >= bound);
+    while (todo) {
+      const int who = __ffs(todo) - 1 + w * 32;
+      todo &= todo - 1;
+      for (int v = v0 + who + lane * kThreads; v < v1; v += 32 * kThreads) {
+        float x[N];
+        L::unpack(__ldg(body + v), x);
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const uint64_t k = make_key(x[j], head + vi * N + j);
-            key = k > key ? k : key;
+        for (int j = 0; j < N; ++j) {
+          if (!(x[j] < bound)) {  // NaN too: it counts as -inf, which may be the bound
+            const uint64_t key = make_key(x[j], head + v * N + j);
+            if (key_value(key) >= bound) {
+              const int at = atomicAdd(&sh.count, 1);
+              if (at < kList) sh.keys[at] = key;
+            }
           }
         }
       }
     }
-    const uint64_t own = key;
-    uint64_t k = warp_sort(key, lane);
-    sh.list[w][lane] = k;
-    __syncthreads();
-#pragma unroll 1
-    for (int n = kWarps / 2; n > 0; n >>= 1) {
-      if (w < n) sh.list[w][lane] = warp_merge(sh.list[w][lane], sh.list[w + n][lane], lane);
-      __syncthreads();
-    }
-    const uint64_t bound = sh.list[0][a.top_n - 1];
-    // the (at most top_n) threads that reach the bound, in order of their place in the list
-    if (own != 0 && own >= bound) {
-      int p = 0;
-      while (sh.list[0][p] != own) ++p;
-      sh.cand[p] = tid;
+    if (edge && key_value(edge) >= bound) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kList) sh.keys[at] = edge;
     }
     __syncthreads();
-    const int n_cand = __popc(__ballot_sync(~0u, lane < a.top_n && sh.list[0][lane] != 0));
-    __syncthreads();
-    uint64_t top = w == 0 ? warp_sort(edge, lane) : 0;
-    for (int c = w; c < n_cand; c += kWarps) {
-      const int who = sh.cand[c];
-      for (int base = v0 + who; base < v1; base += 32 * kThreads) {
-        const int vi = base + lane * kThreads;
+    const int count = sh.count;
+    uint64_t top = 0;
+    if (count <= kList) {
+      for (int c = w * 32; c < count; c += kThreads) {
+        const uint64_t k = warp_sort(c + lane < count ? sh.keys[c + lane] : 0ull, lane);
+        top = c == w * 32 ? k : warp_merge(top, k, lane);
+      }
+    } else {
+      // too many equal entries for the list: all entries, a warp's 32 vectors at a time
+      if (w == 0) top = warp_sort(edge, lane);
+      for (int v = v0 + w * 32; v < v1; v += kThreads) {
         float x[N];
-        if (vi < v1) L::unpack(__ldg(body + vi), x);
+        if (v + lane < v1) L::unpack(__ldg(body + v + lane), x);
+        const uint64_t cut = __shfl_sync(~0u, top, a.top_n - 1);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          uint64_t e = vi < v1 ? make_key(x[j], head + vi * N + j) : 0;
-          if (e < bound) e = 0;
-          if (__any_sync(~0u, e != 0)) top = warp_merge(top, warp_sort(e, lane), lane);
+          const uint64_t k = v + lane < v1 ? make_key(x[j], head + (v + lane) * N + j) : 0;
+          if (__any_sync(~0u, k > cut)) top = warp_merge(top, warp_sort(k, lane), lane);
         }
       }
     }
     sh.list[w][lane] = top;
+    block_merge(sh.list, count > 128 ? kWarps : count > 64 ? 4 : count > 32 ? 2 : 1, w, lane);
+  } else {
     __syncthreads();
-#pragma unroll 1
-    for (int n = kWarps / 2; n > 0; n >>= 1) {
-      if (w < n) sh.list[w][lane] = warp_merge(sh.list[w][lane], sh.list[w + n][lane], lane);
-      __syncthreads();
+  }
+  // this CTA's sums and list, into the first CTA's shared memory
+  if (w == 0) {
+    Sums s{-CUDART_INF_F, 0.f, 0.f};
+    for (int i = 0; i < kWarps; ++i) s = join(s, sh.warp_sums[i]);
+    RowShared* to = &sh;
+    if constexpr (CS > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
+      to = cg::this_cluster().map_shared_rank(&sh, 0);
     }
-    if (w == 0) sh.mine[lane] = sh.list[0][lane];
+    if (a.top_n > 0) to->from[rank][lane] = sh.list[0][lane];
+    if (lane == 0) {
+      to->from_sums[rank] = s;
+      to->from_nan[rank] = sh.nan;
+    }
+  } else if constexpr (CS > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   }
   if constexpr (CS > 1) {
     cg::this_cluster().sync();
   } else {
     __syncthreads();
   }
-  if (rank == 0 && w == 0) {
-    Sums s = sh.sums;
-    int any_nan = sh.nan;
-    uint64_t top = a.top_n > 0 ? sh.mine[lane] : 0;
-    if constexpr (CS > 1) {
-      for (int r = 1; r < CS; ++r) {
-        const RowShared* o = cg::this_cluster().map_shared_rank(&sh, r);
-        s = join(s, o->sums);
-        any_nan |= o->nan;
-        if (a.top_n > 0) top = warp_merge(top, o->mine[lane], lane);
-      }
+  if (rank != 0) return;
+  if (CS > 1 && a.top_n > 0) block_merge(sh.from, CS, w, lane);
+  if (w == 0) {
+    Sums s = sh.from_sums[0];
+    int any_nan = sh.from_nan[0];
+#pragma unroll
+    for (int r = 1; r < CS; ++r) {
+      s = join(s, sh.from_sums[r]);
+      any_nan |= sh.from_nan[r];
     }
     const bool empty = s.m == -CUDART_INF_F, inf = s.m == CUDART_INF_F;
     const float log2s = log2f(s.s);
-    const float off = kLn2 * log2s;  // ln p of an entry x: x - m - off
+    const float off = kLn2 * (log2s - rest(s.m));  // ln p of an entry x: x - m - off
     auto logp = [&](float x) {
       if (inf) return CUDART_NAN_F;
       if (empty || !(x > -CUDART_INF_F)) return -CUDART_INF_F;
@@ -319,18 +441,16 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const ft_logpr
       if (a.status && (any_nan || inf)) atomicOr(a.status, FT_ST_NAN);
       if (a.entropy) a.entropy[t] = inf ? CUDART_NAN_F : empty ? 0.f : kLn2 * (log2s - s.u / s.s);
       if (a.logprob && a.tokens) {
-        const int id = a.tokens[t];
-        if (id >= a.V && a.status) atomicOr(a.status, FT_ST_BAD_TOKEN);
-        a.logprob[t] = id >= 0 && id < a.V ? logp(L::scalar(row + id)) : CUDART_NAN_F;
+        if (token >= a.V && a.status) atomicOr(a.status, FT_ST_BAD_TOKEN);
+        a.logprob[t] = token >= 0 && token < a.V ? logp(token_x) : CUDART_NAN_F;
       }
     }
     if (lane < a.top_n) {
-      if (a.top_ids) a.top_ids[(int64_t)t * a.top_n + lane] = (int32_t)key_id(top);
-      if (a.top_logprobs) a.top_logprobs[(int64_t)t * a.top_n + lane] = logp(key_value(top));
+      const uint64_t top = sh.from[0][lane];
+      a.top_ids[(int64_t)t * a.top_n + lane] = (int32_t)key_id(top);
+      a.top_logprobs[(int64_t)t * a.top_n + lane] = logp(key_value(top));
     }
   }
-  // the first CTA has read the others' shared memory when they leave
-  if constexpr (CS > 1) cg::this_cluster().sync();
 }
 
 template <typename E, int CS>
@@ -350,10 +470,10 @@ cudaError_t launch(const ft_logprob_args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_cs(const ft_logprob_args& a, cudaStream_t st) {
-  // enough CTAs for the machine, but no CTA with less than one batch
+  // enough CTAs for the machine (four to an SM), but no CTA with less than one batch
   const int vecs = a.V / Logit<E>::N;
   int cs = 1;
-  while (cs < 8 && (int64_t)a.T * cs < 4 * sm_count() && vecs / cs > kThreads * kVecs) cs *= 2;
+  while (cs < kMaxCluster && (int64_t)a.T * cs < 4 * sm_count() && vecs / cs > kThreads * kVecs) cs *= 2;
   switch (cs) {
     case 1: return launch<E, 1>(a, st);
     case 2: return launch<E, 2>(a, st);

@@ -16,11 +16,10 @@
 // again with care.
 //
 // Alternatives without a second pass over HBM: each thread keeps only its
-// largest value.  The top_n-th largest of these is a bound that at least top_n
-// entries reach, and only threads whose largest reaches it hold such entries:
-// a warp looks at each such thread's entries again (from L2) and collects those
-// that reach the bound, a little over top_n where few are equal.  They are
-// ordered by a 64-bit key (value, then lower id).  Where they overflow the list
+// largest value.  The top_n-th largest over groups of threads is a bound that
+// at least top_n entries reach, and only threads whose largest reaches it hold
+// such entries: a warp looks at each such thread's entries again (from L2) and
+// collects those that reach the bound, top_n and a few more.  They are ordered by a 64-bit key (value, then lower id).  Where they overflow the list
 // (thousands of equal logits) the warps walk all entries, each merging what
 // beats its own top_n-th.
 //
@@ -226,9 +225,10 @@ struct RowShared {
   uint64_t from[kMaxCluster][kMaxTop];  // the first CTA's: each CTA's best, descending
   Sums from_sums[kMaxCluster];
   int from_nan[kMaxCluster];
-  float best[kWarps][kMaxTop];
+  float best[64];          // largest of each 4 threads
+  uint8_t who[kThreads];   // threads whose largest reaches the bound
   Sums warp_sums[kWarps];
-  int count, nan;
+  int n_who, count, nan;
 };
 
 template <typename E, int CS>
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   const int rank = CS == 1 ? 0 : (int)(blockIdx.x % CS);
   const int t = blockIdx.x / CS;
   const E* row = static_cast<const E*>(a.logits) + (int64_t)t * a.row_stride;
-  if (tid == 0) sh.count = sh.nan = 0;
+  if (tid == 0) sh.n_who = sh.count = sh.nan = 0;
   if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before remote writes
 
   // The given token's logit, on its way while the row is read.
@@ -342,16 +342,29 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   if (__any_sync(~0u, nan) && lane == 0) sh.nan = 1;  // (read after the barriers below)
 
   if (a.top_n > 0) {
-    // the bound: the top_n-th largest of the threads' largest (-inf: fewer threads)
-    sh.best[w][lane] = warp_sort(best == best ? best : -CUDART_INF_F, lane);
-    block_merge(sh.best, kWarps, w, lane);
-    const float bound = sh.best[0][a.top_n - 1];
-    // the entries that reach it
-    unsigned todo = __ballot_sync(~0u, best >= bound);
-    while (todo) {
-      const int who = __ffs(todo) - 1 + w * 32;
-      todo &= todo - 1;
-      for (int v = v0 + who + lane * kThreads; v < v1; v += 32 * kThreads) {
+    // The bound: the top_n-th largest of 64 groups of 4 threads, or 32 of 8 where
+    // that leaves enough groups above it (-inf: fewer groups have vectors).
+    // Of g groups about g ln(g / (g - top_n)) entries reach the bound: 9 for 8
+    // and 22 for 16 of 32, 44 for 32 of 64 (all 32 of 32 would be some 130).
+    float most = best == best ? best : -CUDART_INF_F;
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+    if ((lane & 3) == 0) sh.best[w * 8 + (lane >> 2)] = most;
+    __syncthreads();
+    float order = sh.best[lane], other = sh.best[lane + 32];
+    if (a.top_n <= 16)
+      order = warp_sort(fmaxf(order, other), lane);
+    else
+      order = warp_merge(warp_sort(order, lane), warp_sort(other, lane), lane);
+    const float bound = __shfl_sync(~0u, order, a.top_n - 1);
+    // the threads with entries that reach it, shared out over the warps
+    if (best >= bound) sh.who[atomicAdd(&sh.n_who, 1)] = (uint8_t)tid;
+    __syncthreads();
+    const int n_who = sh.n_who;
+    for (int c = w; c < n_who; c += kWarps) {
+      const int first = v0 + sh.who[c];
+#pragma unroll 2
+      for (int v = first + lane * kThreads; v < v1; v += 32 * kThreads) {
         float x[N];
         L::unpack(__ldg(body + v), x);
 #pragma unroll
@@ -370,17 +383,21 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
       const int at = atomicAdd(&sh.count, 1);
       if (at < kList) sh.keys[at] = edge;
     }
+    if (tid < kMaxTop) sh.list[0][tid] = 0;
     __syncthreads();
     const int count = sh.count;
-    uint64_t top = 0;
     if (count <= kList) {
-      for (int c = w * 32; c < count; c += kThreads) {
-        const uint64_t k = warp_sort(c + lane < count ? sh.keys[c + lane] : 0ull, lane);
-        top = c == w * 32 ? k : warp_merge(top, k, lane);
+      // each key's place is how many are larger
+      for (int i = tid; i < count; i += kThreads) {
+        const uint64_t key = sh.keys[i];
+        int place = 0;
+        for (int j = 0; j < count; ++j) place += sh.keys[j] > key;
+        if (place < a.top_n) sh.list[0][place] = key;
       }
+      __syncthreads();
     } else {
       // too many equal entries for the list: all entries, a warp's 32 vectors at a time
-      if (w == 0) top = warp_sort(edge, lane);
+      uint64_t top = w == 0 ? warp_sort(edge, lane) : 0;
       for (int v = v0 + w * 32; v < v1; v += kThreads) {
         float x[N];
         if (v + lane < v1) L::unpack(__ldg(body + v + lane), x);
@@ -391,16 +408,17 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
           if (__any_sync(~0u, k > cut)) top = warp_merge(top, warp_sort(k, lane), lane);
         }
       }
+      sh.list[w][lane] = top;
+      block_merge(sh.list, kWarps, w, lane);
     }
-    sh.list[w][lane] = top;
-    block_merge(sh.list, count > 128 ? kWarps : count > 64 ? 4 : count > 32 ? 2 : 1, w, lane);
   } else {
     __syncthreads();
   }
   // this CTA's sums and list, into the first CTA's shared memory
   if (w == 0) {
-    Sums s{-CUDART_INF_F, 0.f, 0.f};
-    for (int i = 0; i < kWarps; ++i) s = join(s, sh.warp_sums[i]);
+    Sums s = sh.warp_sums[lane % kWarps];
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) s = join(s, Sums{__shfl_xor_sync(~0u, s.m, o), __shfl_xor_sync(~0u, s.s, o), __shfl_xor_sync(~0u, s.u, o)});
     RowShared* to = &sh;
     if constexpr (CS > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started

@@ -14,6 +14,7 @@
 // one it needs, instead of reading another launch's sums: requests are a few
 // thousand at most and their lengths stay in L2.
 #include "attn_side.h"
+#include "tma.h"
 
 namespace ft {
 namespace {
@@ -57,6 +58,8 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const ft_plan_args a,
   uint32_t fault = 0;
 
   rec_req[tid] = -1;
+  pdl_wait();
+  pdl_trigger();
   if (a.parents) s_parent[tid] = t < a.max_tokens ? a.parents[t] : -1;
   const int free_count = *a.free_count;
   __syncthreads();
@@ -209,8 +212,10 @@ extern "C" int ft_kv_plan(const ft_plan_args* args, void* stream) {
   int log2_page = 0;
   while ((1 << log2_page) < a.page_size) ++log2_page;
   const int grid = a.max_tokens > 0 ? (a.max_tokens + kThreads - 1) / kThreads : 1;
-  kv_plan_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, log2_page);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(cfg, attr, dim3(grid), dim3(kThreads), 0, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, a, log2_page);
   if (e != cudaSuccess) return record_error(FT_E_CUDA, "plan launch failed: %s", cudaGetErrorString(e));
   return FT_OK;
 }

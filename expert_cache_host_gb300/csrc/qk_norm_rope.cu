@@ -5,14 +5,20 @@
 //   token's angles; all in fp32, one rounding at the end.
 //
 // Every element is read and written once, so HBM bounds it (latency, for a
-// few tokens).  A head is D/8 lanes with 8 elements each: a row is loaded and
-// stored in 16-byte pieces, the mean is a shuffle sum over the head's lanes,
-// and with the halves paired (i with i + rot/2) a lane's partner elements are
-// the same 8 places of one other lane, which one shuffle per element fetches.  A
-// warp takes HPW = 256/D heads at a time and ITER such groups of one token, so
-// the token's angles are loaded once for ITER*HPW heads and ITER 16-byte loads
-// per lane are in flight before the first is used.
+// few tokens) if the instructions per element stay few.  A head is D/8 lanes
+// with 8 elements each; the mean is a shuffle sum over the head's lanes.  A
+// warp takes HPW = 256/D heads at a time and ITER such sets of one token, so
+// that the token's angles and the weights are loaded once for ITER*HPW heads
+// and ITER 16-byte loads per lane are in flight before the first is used.
+//
+// With the whole head rotated in halves (i with i + D/2) a lane holds both
+// members of its pairs: elements 4l..4l+3 of either half.  The weights then go
+// into the angles once per token, y_a = r (x_a (w_a c) - x_b (w_b s)), and an
+// element costs 1.5 packed fp32 operations beside its conversions.  Otherwise
+// a lane holds 8 neighbours, and a partner half is another lane's 8 (a shuffle
+// each).
 #include "attn_side.h"
+#include "tma.h"
 
 namespace ft {
 namespace {
@@ -28,164 +34,212 @@ struct Args {
   bool vec_in, vec_out;  // rows of q, k, v / q_out are 16-byte aligned
 };
 
-__device__ __forceinline__ uint4 load8(const uint16_t* p, bool vec) {
-  if (vec) return *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ uint4 load8(const uint16_t* lo, const uint16_t* hi, bool split, bool vec) {
+  if (vec) {
+    if (!split) return *reinterpret_cast<const uint4*>(lo);
+    const uint2 a = *reinterpret_cast<const uint2*>(lo), b = *reinterpret_cast<const uint2*>(hi);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
+  for (int i = 0; i < 4; ++i) {
+    const uint16_t* p = (i < 2 ? lo + 2 * i : hi + 2 * (i - 2));
+    w[i] = (uint32_t)p[0] | ((uint32_t)p[1] << 16);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, uint4 v, bool vec) {
+__device__ __forceinline__ void store8(uint16_t* lo, uint16_t* hi, uint4 v, bool split, bool vec) {
   if (vec) {
-    *reinterpret_cast<uint4*>(p) = v;
+    if (!split) {
+      *reinterpret_cast<uint4*>(lo) = v;
+    } else {
+      *reinterpret_cast<uint2*>(lo) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2*>(hi) = make_uint2(v.z, v.w);
+    }
     return;
   }
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    p[2 * i] = (uint16_t)w[i];
-    p[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    uint16_t* p = (i < 2 ? lo + 2 * i : hi + 2 * (i - 2));
+    p[0] = (uint16_t)w[i];
+    p[1] = (uint16_t)(w[i] >> 16);
   }
 }
 
-template <typename E, int D, int ITER>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const __grid_constant__ Args g) {
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+template <typename E>
+__device__ __forceinline__ float4 weights4(const void* w, int at) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at));
+  const float2 a = Elem<E>::unpack(v.x), b = Elem<E>::unpack(v.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// HALVES: the whole head rotated, i with i + D/2.
+template <typename E, int D, int ITER, bool HALVES>
+__global__ void __launch_bounds__(kWarps * 32, ITER == 1 ? 1 : HALVES ? 5 : 3) qk_norm_rope_kernel(const __grid_constant__ Args g) {
   constexpr int LPH = D / 8;      // lanes per head
   constexpr int HPW = 32 / LPH;   // heads per warp at a time
   const ft_qk_args& a = g.a;
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, sub = lane % LPH;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t64 = unit / g.groups;
   if (t64 >= a.T) return;
   const int t = (int)t64, group = (int)(unit - t64 * g.groups);
   const int Hq = a.q_heads, Hkv = a.cache.kv_heads;
+  // this lane's elements of a head: 4 at e0 and 4 at e1
+  const int e0 = HALVES ? sub * 4 : sub * 8, e1 = HALVES ? D / 2 + sub * 4 : sub * 8 + 4;
 
   const int pos = a.positions[t];
   const int64_t slot = a.slots[t];
+  const int h0 = group * ITER * HPW + lane / LPH;
   uint4 raw[ITER];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + t * a.q_stride;
+    const uint16_t* k = static_cast<const uint16_t*>(a.k) + t * a.k_stride - (int64_t)Hq * D;
+    const uint16_t* v = static_cast<const uint16_t*>(a.v) + t * a.v_stride - (int64_t)(Hq + Hkv) * D;
 #pragma unroll
-  for (int it = 0; it < ITER; ++it) {
-    const int h = (group * ITER + it) * HPW + lane / LPH;
-    if (h < g.heads) {
-      const uint16_t* row;
-      if (h < Hq)
-        row = static_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)h * D;
-      else if (h < Hq + Hkv)
-        row = static_cast<const uint16_t*>(a.k) + t * a.k_stride + (int64_t)(h - Hq) * D;
-      else
-        row = static_cast<const uint16_t*>(a.v) + t * a.v_stride + (int64_t)(h - Hq - Hkv) * D;
-      raw[it] = load8(row + sub * 8, g.vec_in);
-    } else {
-      raw[it] = make_uint4(0, 0, 0, 0);
+    for (int it = 0; it < ITER; ++it) {
+      const int h = h0 + it * HPW;
+      if (h < g.heads) {
+        const uint16_t* row = (h < Hq ? q : h < Hq + Hkv ? k : v) + (int64_t)h * D;
+        raw[it] = load8(row + e0, row + e1, HALVES, g.vec_in);
+      } else {
+        raw[it] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
+  bool for_keys = h0 >= Hq;  // whose weights are in wa, wb
+  float4 wa = weights4<E>(for_keys ? a.k_weight : a.q_weight, e0);
+  float4 wb = weights4<E>(for_keys ? a.k_weight : a.q_weight, e1);
   const bool in_range = pos >= 0 && pos < a.max_pos;
   const bool keep = in_range && slot >= 0 && slot < g.num_slots;  // keys and values are written
   if (a.status && group == 0 && lane == 0) {
     if (!in_range) atomicOr(a.status, FT_ST_BAD_TOKEN);
     if (slot >= g.num_slots) atomicOr(a.status, FT_ST_BAD_SLOT);
   }
-  const int64_t page = slot >> g.log2_page;
-  const int64_t row_in = slot & ((int64_t(1) << g.log2_page) - 1);
+  const int64_t page = keep ? slot >> g.log2_page : 0;
+  const int64_t row_in = keep ? slot & ((int64_t(1) << g.log2_page) - 1) : 0;
+  uint16_t* const q_out = static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride;
+  uint16_t* const k_out = static_cast<uint16_t*>(a.cache.k) + page * a.cache.k_page_stride + row_in * a.cache.k_token_stride;
+  uint16_t* const v_out = static_cast<uint16_t*>(a.cache.v) + page * a.cache.v_page_stride + row_in * a.cache.v_token_stride;
 
-  // The angles of this lane's 8 elements.  Halves paired: element i < rot/2
-  // and i + rot/2 share angle i; neighbours paired: 2i and 2i+1 share angle i.
-  const int half = a.rot_dim / 2, e0 = sub * 8;
-  const bool rotated = e0 < a.rot_dim;  // rot_dim is a multiple of 16: a lane's 8 elements are on one side
-  const bool upper = e0 >= half;        // halves: this lane holds the second member of its pairs
-  float cs[8], sn[8];
+  // The angles and weights of this lane's elements.  Halves paired: element
+  // i < rot/2 and i + rot/2 share angle i; neighbours paired: 2i and 2i+1 do.
+  const int half = a.rot_dim / 2;
+  const bool rotated = HALVES || sub * 8 < a.rot_dim;  // rot_dim is a multiple of 16: a lane's 8 are on one side
+  const bool upper = !HALVES && sub * 8 >= half;       // this lane holds the second members of its pairs
+  const float* angles = a.cos_sin + (int64_t)(in_range ? pos : 0) * a.rot_dim;
+  float cs[8], sn[8];  // HALVES: w_a c, w_b c and w_a s, w_b s of one weight vector (set per head type)
+  float4 c4, s4;
+  if constexpr (HALVES) {
+    c4 = __ldg(reinterpret_cast<const float4*>(angles + e0));
+    s4 = __ldg(reinterpret_cast<const float4*>(angles + half + e0));
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  if (rotated && in_range) {
-    const float* base = a.cos_sin + (int64_t)pos * a.rot_dim;
-    if (a.interleaved) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(base + sub * 4));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(base + half + sub * 4));
-      cs[0] = cs[1] = c.x, cs[2] = cs[3] = c.y, cs[4] = cs[5] = c.z, cs[6] = cs[7] = c.w;
-      sn[0] = sn[1] = s.x, sn[2] = sn[3] = s.y, sn[4] = sn[5] = s.z, sn[6] = sn[7] = s.w;
-    } else {
-      const float* p = base + (upper ? e0 - half : e0);
+    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+    if (rotated) {
+      if (a.interleaved) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(angles + sub * 4));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(angles + half + sub * 4));
+        cs[0] = cs[1] = c.x, cs[2] = cs[3] = c.y, cs[4] = cs[5] = c.z, cs[6] = cs[7] = c.w;
+        sn[0] = sn[1] = s.x, sn[2] = sn[3] = s.y, sn[4] = sn[5] = s.z, sn[6] = sn[7] = s.w;
+      } else {
+        const float* p = angles + (upper ? sub * 8 - half : sub * 8);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(p) + v);
-        const float4 s = __ldg(reinterpret_cast<const float4*>(p + half) + v);
-        cs[4 * v] = c.x, cs[4 * v + 1] = c.y, cs[4 * v + 2] = c.z, cs[4 * v + 3] = c.w;
-        sn[4 * v] = s.x, sn[4 * v + 1] = s.y, sn[4 * v + 2] = s.z, sn[4 * v + 3] = s.w;
+        for (int v = 0; v < 2; ++v) {
+          const float4 c = __ldg(reinterpret_cast<const float4*>(p) + v);
+          const float4 s = __ldg(reinterpret_cast<const float4*>(p + half) + v);
+          cs[4 * v] = c.x, cs[4 * v + 1] = c.y, cs[4 * v + 2] = c.z, cs[4 * v + 3] = c.w;
+          sn[4 * v] = s.x, sn[4 * v + 1] = s.y, sn[4 * v + 2] = s.z, sn[4 * v + 3] = s.w;
+        }
       }
     }
   }
   // the lane of this head with the paired elements (itself where neighbours are paired)
   const int hop = half / 8;
   const int mate = lane - sub + (a.interleaved || !rotated ? sub : (upper ? sub - hop : sub + hop));
-  const uint4 wq = __ldg(reinterpret_cast<const uint4*>(a.q_weight) + sub);
-  const uint4 wk = __ldg(reinterpret_cast<const uint4*>(a.k_weight) + sub);
-
 #pragma unroll
   for (int it = 0; it < ITER; ++it) {
-    const int h = (group * ITER + it) * HPW + lane / LPH;
-    const uint32_t rw[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
-    float x[8];
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Elem<E>::unpack(rw[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-      ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
-    }
-#pragma unroll
-    for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-    const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-    const uint4 w4 = h < Hq ? wq : wk;
-    const uint32_t ww[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Elem<E>::unpack(ww[i]);
-      x[2 * i] *= r * f.x;
-      x[2 * i + 1] *= r * f.y;
-    }
-    float y[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        y[i] = x[i] * cs[i] - x[i + 1] * sn[i];
-        y[i + 1] = x[i + 1] * cs[i] + x[i] * sn[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = __shfl_sync(~0u, x[i], mate);
-        y[i] = upper ? fmaf(x[i], cs[i], m * sn[i]) : fmaf(x[i], cs[i], -m * sn[i]);
-      }
-    }
-    if (!rotated) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i];
-    }
+    const int h = h0 + it * HPW;
     uint4 o = raw[it];
-    if (h < Hq + Hkv) {
-      o.x = Elem<E>::pack(y[0], y[1]);
-      o.y = Elem<E>::pack(y[2], y[3]);
-      o.z = Elem<E>::pack(y[4], y[5]);
-      o.w = Elem<E>::pack(y[6], y[7]);
+    if (h0 - lane / LPH + it * HPW < Hq + Hkv) {  // (warp-uniform: not a set of values alone)
+      const bool key = h >= Hq;
+      if (key != for_keys) {
+        for_keys = key;
+        wa = weights4<E>(key ? a.k_weight : a.q_weight, e0);
+        wb = weights4<E>(key ? a.k_weight : a.q_weight, e1);
+      }
+      const uint32_t rw[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+      float x[8];
+      float ss = 0.f, st = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = Elem<E>::unpack(rw[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+        ss = fmaf(f.x, f.x, ss);
+        st = fmaf(f.y, f.y, st);
+      }
+      ss += st;
+#pragma unroll
+      for (int p = 1; p < LPH; p <<= 1) ss += __shfl_xor_sync(~0u, ss, p);
+      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      float y[8];
+      if constexpr (HALVES) {
+        const float4 ac = mul4(wa, c4), bs = mul4(wb, s4), bc = mul4(wb, c4), as = mul4(wa, s4);
+        y[0] = (x[0] * ac.x - x[4] * bs.x) * r, y[4] = (x[4] * bc.x + x[0] * as.x) * r;
+        y[1] = (x[1] * ac.y - x[5] * bs.y) * r, y[5] = (x[5] * bc.y + x[1] * as.y) * r;
+        y[2] = (x[2] * ac.z - x[6] * bs.z) * r, y[6] = (x[6] * bc.z + x[2] * as.z) * r;
+        y[3] = (x[3] * ac.w - x[7] * bs.w) * r, y[7] = (x[7] * bc.w + x[3] * as.w) * r;
+      } else {
+        const float w8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= r * w8[i];
+        if (a.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            y[i] = x[i] * cs[i] - x[i + 1] * sn[i];
+            y[i + 1] = x[i + 1] * cs[i] + x[i] * sn[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float m = __shfl_sync(~0u, x[i], mate);
+            y[i] = upper ? fmaf(x[i], cs[i], m * sn[i]) : fmaf(x[i], cs[i], -m * sn[i]);
+          }
+        }
+        if (!rotated) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = x[i];
+        }
+      }
+      if (h < Hq + Hkv) {
+        o.x = Elem<E>::pack(y[0], y[1]);
+        o.y = Elem<E>::pack(y[2], y[3]);
+        o.z = Elem<E>::pack(y[4], y[5]);
+        o.w = Elem<E>::pack(y[6], y[7]);
+      }
     }
     if (h < Hq) {
       if (!in_range) o = make_uint4(0, 0, 0, 0);
-      store8(static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + (int64_t)h * D + e0, o, g.vec_out);
+      uint16_t* dst = q_out + (int64_t)h * D;
+      store8(dst + e0, dst + e1, o, HALVES, g.vec_out);
     } else if (h < g.heads && keep) {
       const bool is_k = h < Hq + Hkv;
-      const int kh = h - Hq - (is_k ? 0 : Hkv);
-      uint16_t* dst = static_cast<uint16_t*>(is_k ? a.cache.k : a.cache.v) +
-                      page * (is_k ? a.cache.k_page_stride : a.cache.v_page_stride) +
-                      row_in * (is_k ? a.cache.k_token_stride : a.cache.v_token_stride) +
-                      kh * (is_k ? a.cache.k_head_stride : a.cache.v_head_stride) + e0;
-      *reinterpret_cast<uint4*>(dst) = o;
+      uint16_t* dst = is_k ? k_out + (int64_t)(h - Hq) * a.cache.k_head_stride
+                           : v_out + (int64_t)(h - Hq - Hkv) * a.cache.v_head_stride;
+      store8(dst + e0, dst + e1, o, HALVES, true);
     }
   }
 }
 
-template <typename E, int D>
+template <typename E, int D, bool HALVES>
 cudaError_t launch(Args g, cudaStream_t st) {
   constexpr int HPW = 32 / (D / 8);
   const int sets = (g.heads + HPW - 1) / HPW;  // warp-wide sets of heads per token
@@ -198,19 +252,24 @@ cudaError_t launch(Args g, cudaStream_t st) {
   const int64_t units = (int64_t)g.a.T * g.groups;
   const int64_t grid = (units + kWarps - 1) / kWarps;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (many)
-    qk_norm_rope_kernel<E, D, 4><<<(unsigned)grid, kWarps * 32, 0, st>>>(g);
-  else
-    qk_norm_rope_kernel<E, D, 1><<<(unsigned)grid, kWarps * 32, 0, st>>>(g);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(cfg, attr, dim3((unsigned)grid), dim3(kWarps * 32), 0, st);
+  return many ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<E, D, 4, HALVES>, g)
+              : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<E, D, 1, HALVES>, g);
+}
+
+template <typename E, int D>
+cudaError_t launch_r(const Args& g, cudaStream_t st) {
+  return g.a.rot_dim == D && !g.a.interleaved ? launch<E, D, true>(g, st) : launch<E, D, false>(g, st);
 }
 
 template <typename E>
 cudaError_t launch_d(const Args& g, cudaStream_t st) {
   switch (g.a.cache.head_dim) {
-    case 64: return launch<E, 64>(g, st);
-    case 128: return launch<E, 128>(g, st);
-    default: return launch<E, 256>(g, st);
+    case 64: return launch_r<E, 64>(g, st);
+    case 128: return launch_r<E, 128>(g, st);
+    default: return launch_r<E, 256>(g, st);
   }
 }
 

@@ -30,6 +30,7 @@
 #include <math_constants.h>
 
 #include "attn_side.h"
+#include "tma.h"
 
 namespace ft {
 namespace {
@@ -237,6 +238,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   constexpr int N = L::N;
   __shared__ RowShared sh;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
   const int rank = CS == 1 ? 0 : (int)(blockIdx.x % CS);
   const int t = blockIdx.x / CS;
   const E* row = static_cast<const E*>(a.logits) + (int64_t)t * a.row_stride;
@@ -477,12 +480,14 @@ cudaError_t launch(const ft_logprob_args& a, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)a.T * CS);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CS;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CS > 1 ? 1 : 0;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<E, CS>, a);
 }
 

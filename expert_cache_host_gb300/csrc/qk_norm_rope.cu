@@ -23,7 +23,7 @@
 namespace ft {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct Args {
   ft_qk_args a;
@@ -80,17 +80,16 @@ __device__ __forceinline__ float4 weights4(const void* w, int at) {
 
 // HALVES: the whole head rotated, i with i + D/2.
 template <typename E, int D, int ITER, bool HALVES>
-__global__ void __launch_bounds__(kWarps * 32, ITER == 1 ? 1 : HALVES ? 5 : 3) qk_norm_rope_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kWarps * 32, ITER == 1 ? 1 : HALVES ? 9 : 6) qk_norm_rope_kernel(const __grid_constant__ Args g) {
   constexpr int LPH = D / 8;      // lanes per head
   constexpr int HPW = 32 / LPH;   // heads per warp at a time
   const ft_qk_args& a = g.a;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, sub = lane % LPH;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t64 = unit / g.groups;
-  if (t64 >= a.T) return;
-  const int t = (int)t64, group = (int)(unit - t64 * g.groups);
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = (int)(unit / (uint32_t)g.groups), group = (int)(unit - (uint32_t)t * g.groups);
+  if (t >= a.T) return;
   const int Hq = a.q_heads, Hkv = a.cache.kv_heads;
   // this lane's elements of a head: 4 at e0 and 4 at e1
   const int e0 = HALVES ? sub * 4 : sub * 8, e1 = HALVES ? D / 2 + sub * 4 : sub * 8 + 4;
@@ -189,14 +188,16 @@ __global__ void __launch_bounds__(kWarps * 32, ITER == 1 ? 1 : HALVES ? 5 : 3) q
       ss += st;
 #pragma unroll
       for (int p = 1; p < LPH; p <<= 1) ss += __shfl_xor_sync(~0u, ss, p);
-      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
       float y[8];
       if constexpr (HALVES) {
         const float4 ac = mul4(wa, c4), bs = mul4(wb, s4), bc = mul4(wb, c4), as = mul4(wa, s4);
-        y[0] = (x[0] * ac.x - x[4] * bs.x) * r, y[4] = (x[4] * bc.x + x[0] * as.x) * r;
-        y[1] = (x[1] * ac.y - x[5] * bs.y) * r, y[5] = (x[5] * bc.y + x[1] * as.y) * r;
-        y[2] = (x[2] * ac.z - x[6] * bs.z) * r, y[6] = (x[6] * bc.z + x[2] * as.z) * r;
-        y[3] = (x[3] * ac.w - x[7] * bs.w) * r, y[7] = (x[7] * bc.w + x[3] * as.w) * r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= r;
+        y[0] = fmaf(x[0], ac.x, -x[4] * bs.x), y[4] = fmaf(x[4], bc.x, x[0] * as.x);
+        y[1] = fmaf(x[1], ac.y, -x[5] * bs.y), y[5] = fmaf(x[5], bc.y, x[1] * as.y);
+        y[2] = fmaf(x[2], ac.z, -x[6] * bs.z), y[6] = fmaf(x[6], bc.z, x[2] * as.z);
+        y[3] = fmaf(x[3], ac.w, -x[7] * bs.w), y[7] = fmaf(x[7], bc.w, x[3] * as.w);
       } else {
         const float w8[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
@@ -246,12 +247,12 @@ cudaError_t launch(Args g, cudaStream_t st) {
   // Few tokens: one set per warp, so that a token spreads over the machine
   // (latency).  Many: four, so that angles and weights are loaded once for
   // four and four loads per lane are in flight.
-  const bool many = (int64_t)g.a.T * sets >= (int64_t)sm_count() * kWarps * 8;
+  const bool many = (int64_t)g.a.T * sets >= (int64_t)sm_count() * 64;
   const int iter = many ? 4 : 1;
   g.groups = (sets + iter - 1) / iter;
   const int64_t units = (int64_t)g.a.T * g.groups;
   const int64_t grid = (units + kWarps - 1) / kWarps;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (units > 0x7FFFFF00) return cudaErrorInvalidValue;  // (refused before: T is limited)
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pdl_config(cfg, attr, dim3((unsigned)grid), dim3(kWarps * 32), 0, st);
@@ -282,6 +283,8 @@ extern "C" int ft_qk_norm_rope(const ft_qk_args* args, void* stream) {
   const ft_qk_args& a = *args;
   if (int rc = check_kv_cache(a.cache, true)) return rc;
   if (a.T < 0 || a.q_heads < 1 || a.max_pos < 1) return record_error(FT_E_ARG, "bad T, q_heads or max_pos");
+  if ((int64_t)a.T * ((int64_t)a.q_heads + 2 * (int64_t)a.cache.kv_heads) > 0x7FFFFF00)
+    return record_error(FT_E_ARG, "T times the heads must stay below 2^31");
   if (!a.q || !a.k || !a.v || !a.q_weight || !a.k_weight || !a.positions || !a.slots || !a.q_out ||
       (!a.cos_sin && a.rot_dim))
     return record_error(FT_E_ARG, "null pointer");

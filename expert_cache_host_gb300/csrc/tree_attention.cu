@@ -37,6 +37,7 @@
 // warp passes it on to `full`.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_side.h"
@@ -202,6 +203,13 @@ struct Walk {
   __device__ __forceinline__ int tile_of(int s, int j) const { return pair ? t0 + j : t0 + 2 * j + s; }
 };
 
+// a / b.  Below 2^21 through fp32: (a + 1/2) / b is at least 1/(2b) from a whole
+// number and the quotient's error is below 2^-22 a / b.  (An integer division is
+// some hundred cycles, several in a row at the head of every CTA.)
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
+  return (a | b) < (1u << 21) ? (uint32_t)__fdividef((float)a + 0.5f, (float)b) : a / b;
+}
+
 // Units are dealt to `grid` CTAs in order, `per` each and one more to the first `extra`.
 struct Deal {
   int per, extra, grid;
@@ -210,13 +218,13 @@ struct Deal {
     // first and last has a tile of it (the join counts on that).
     const uint32_t t = (uint32_t)min(total, 0x7FFFFFFFll);  // more than 2^31 units: the last CTA takes what is left
     grid = max(1, min(ctas, (int)(t / kPairUnits)));
-    per = (int)(t / (uint32_t)grid);
+    per = (int)quotient(t, grid);
     extra = (int)(t - (uint32_t)per * grid);
   }
   __device__ __forceinline__ long long first(int c) const { return (long long)c * per + min(c, extra); }
   __device__ __forceinline__ int owner(long long unit) const {
     const uint32_t u = (uint32_t)min(unit, 0x7FFFFFFFll), wide = (uint32_t)extra * (per + 1);
-    const int c = u < wide ? (int)(u / (uint32_t)(per + 1)) : extra + (int)((u - wide) / (uint32_t)max(per, 1));
+    const int c = u < wide ? (int)quotient(u, per + 1) : extra + (int)quotient(u - wide, max(per, 1));
     return min(c, grid - 1);
   }
 };
@@ -236,11 +244,11 @@ struct Shared {
 };
 
 // The 32 bits of a token's visibility that begin at new token `off` (bits
-// before token 0 are the context: set).
-__device__ __forceinline__ uint32_t mask_bits(const Args& g, const uint32_t* row, int i, int off) {
+// before token 0 are the context: set).  `first`: the row's first two words.
+__device__ __forceinline__ uint32_t mask_bits(const Args& g, const uint32_t* row, uint2 first, int i, int off) {
   if (off <= -32) return ~0u;
   auto word = [&](int w) -> uint32_t {
-    if (row) return w < g.a.mask_words ? row[w] : 0u;
+    if (row) return w >= g.a.mask_words ? 0u : w == 0 ? first.x : w == 1 ? first.y : row[w];
     const int left = i + 1 - 32 * w;  // without a mask: tokens 0 .. i
     return left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
   };
@@ -250,11 +258,11 @@ __device__ __forceinline__ uint32_t mask_bits(const Args& g, const uint32_t* row
 }
 
 // Which of the 32 keys from key0 on row i of the request sees.
-__device__ __forceinline__ uint32_t visible(const Args& g, const Req& r, const uint32_t* row, int i, int key0, int w,
+__device__ __forceinline__ uint32_t visible(const Args& g, const Req& r, const uint32_t* row, uint2 first, int i, int key0, int w,
                                             uint32_t pages) {
   const int off = key0 - r.ctx, left = r.n - off;
   if (left <= 0) return 0;
-  uint32_t v = mask_bits(g, row, i, off);
+  uint32_t v = mask_bits(g, row, first, i, off);
   if (left < 32) v &= (1u << left) - 1;
   // pages of the tile, in groups of min(page_size, 32) keys
   const int per = 1 << g.log2_page;
@@ -341,7 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane == NST + 2) {
       mbar_init(&sh.q_full, 1);
       mbar_init(&sh.q_empty, 1);
-      sh.start.left = 0;
     }
     mbar_init_fence();
     if (lane < 3) prefetch_map(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v);
@@ -350,17 +357,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();  // the join kernel may be set up; it waits for this grid's end
 
-  // Total work and where this CTA's share begins: inclusive sums of the
-  // requests' units over the block, kThreads requests at a time; with no more
-  // requests than that, one pass serves both uses.
-  long long total = 0, lo;  // units of all items; the first of this CTA's share
+  // Total work and where this CTA's share begins, from inclusive sums of the
+  // requests' units: by warp 0 where its lanes hold all requests, else over the
+  // block, kThreads requests at a time.
+  long long total = 0, lo = 0;  // units of all items; the first of this CTA's share (warp 0 knows)
   Deal deal(0, 1);
   {
+    const int c = blockIdx.x;
+    auto share_of = [&] {
+      deal = Deal(total, gridDim.x);
+      lo = deal.first(c);
+      return c >= deal.grid ? 0 : c == deal.grid - 1 ? (int)min(total - lo, 0x7FFFFFFFll) : deal.per + (c < deal.extra);
+    };
+    // The walk's start, `at` units into request b.  (A request of more than 2^32
+    // units does not occur: 2^31 keys are 2^24 tiles.)
+    auto place = [&](Walk& w, const Req& r, int b, uint32_t at) {
+      const uint32_t per_head = (uint32_t)head_units(g, r), per_block = (uint32_t)r.tiles * kPairUnits + kItemUnits;
+      w.b = b;
+      w.r = r;
+      w.h = (int)quotient(at, per_head);
+      const uint32_t in_head = at - w.h * per_head;
+      w.blk = min((int)quotient(in_head, per_block), r.blocks - 1);
+      w.unit = (int)(in_head - w.blk * per_block);
+    };
     Req r{};
     long long u = 0, x = 0;
-    auto scan = [&](int b0) {
+    auto warp_scan = [&](int b) {
       r = Req{};
-      if (b0 + tid < a.num_reqs) r = request(g, b0 + tid);
+      if (b < a.num_reqs) r = request(g, b);
       u = head_units(g, r) * a.cache.kv_heads;
       x = u;
 #pragma unroll
@@ -368,42 +392,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long y = __shfl_up_sync(~0u, x, o);
         if (lane >= o) x += y;
       }
-      __syncthreads();
-      if (lane == 31) sh.red[warp] = x;
-      __syncthreads();
-      long long all = 0, before = 0;
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const long long y = sh.red[w];
-        if (w < warp) before += y;
-        all += y;
-      }
-      x += before;
-      return all;
     };
-    for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) total += scan(b0);
-    deal = Deal(total, gridDim.x);
-    const int c = blockIdx.x;
-    lo = deal.first(c);
-    const int share = c >= deal.grid ? 0 : c == deal.grid - 1 ? (int)min(total - lo, 0x7FFFFFFFll) : deal.per + (c < deal.extra);
-    long long base = 0;
-    for (int b0 = 0; b0 < a.num_reqs && base <= lo; b0 += kThreads) {
-      const long long all = a.num_reqs > kThreads ? scan(b0) : total;
-      const long long first = base + x - u;
-      if (share > 0 && lo >= first && lo < first + u) {
-        // (a request of more than 2^32 units does not occur: 2^31 keys are 2^24 tiles)
-        const uint32_t at = (uint32_t)(lo - first), per_head = (uint32_t)head_units(g, r);
-        const uint32_t per_block = (uint32_t)r.tiles * kPairUnits + kItemUnits;
-        Walk& w = sh.start;
-        w.left = share;
-        w.b = b0 + tid;
-        w.r = r;
-        w.h = (int)(at / per_head);
-        const uint32_t in_head = at - w.h * per_head;
-        w.blk = min((int)(in_head / per_block), r.blocks - 1);
-        w.unit = (int)(in_head - w.blk * per_block);
+    if (a.num_reqs <= 32) {
+      if (warp == 0) {
+        warp_scan(lane);
+        total = __shfl_sync(~0u, x, 31);
+        const int share = share_of();
+        if (share > 0 && lo >= x - u && lo < x) place(sh.start, r, lane, (uint32_t)(lo - (x - u)));
+        if (lane == 0) sh.start.left = share;
       }
-      base += all;
+    } else {
+      auto scan = [&](int b0) {
+        warp_scan(b0 + tid);
+        __syncthreads();
+        if (lane == 31) sh.red[warp] = x;
+        __syncthreads();
+        long long all = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+          const long long y = sh.red[w];
+          if (w < warp) before += y;
+          all += y;
+        }
+        x += before;
+        return all;
+      };
+      for (int b0 = 0; b0 < a.num_reqs; b0 += kThreads) total += scan(b0);
+      const int share = share_of();
+      long long base = 0;
+      for (int b0 = 0; b0 < a.num_reqs && base <= lo; b0 += kThreads) {
+        const long long all = a.num_reqs > kThreads ? scan(b0) : total;
+        const long long first = base + x - u;
+        if (share > 0 && lo >= first && lo < first + u) place(sh.start, r, b0 + tid, (uint32_t)(lo - first));
+        base += all;
+      }
+      if (tid == 0) sh.start.left = share;
     }
     tc_fence_before();
     __syncthreads();
@@ -596,6 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = tok < g.tpt && i < r.n;
       const bool warp_live = __any_sync(~0u, valid);
       const uint32_t* mrow = a.mask ? a.mask + (int64_t)(r.q0 + (valid ? i : 0)) * a.mask_words : nullptr;
+      uint2 first = make_uint2(0, 0);  // (loaded while the tiles are on their way)
+      if (mrow && wk.t1 * KT > r.ctx) {
+        first.x = mrow[0];
+        if (a.mask_words > 1) first.y = mrow[1];
+      }
       const int cnt = wk.count(s);
       float m = -CUDART_INF_F, l = 0.f;
       for (int j = 0; j < cnt; ++j, ++tiles_done) {
@@ -616,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((t + 1) * KT > r.ctx || pages != full_pages) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t vis = valid ? visible(g, r, mrow, i, t * KT + w * 32, w, pages) : 0u;
+              const uint32_t vis = valid ? visible(g, r, mrow, first, i, t * KT + w * 32, w, pages) : 0u;
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 if (!(vis >> c & 1)) x[w * 32 + c] = -CUDART_INF_F;
@@ -680,9 +708,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool nonfinite = wk.t1 * KT > r.ctx && sh.nonfinite[item & 3];  // (written where an item has new keys)
       // Rows' output: with a row tile per stream the thread's own; else the two
       // streams' halves of the keys joined, each warpgroup half of the columns.
-      float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + log2f(l) : -CUDART_INF_F;
+      float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + __log2f(l) : -CUDART_INF_F;
       int c0 = 0, c1 = D;
-      float inv = lse == -CUDART_INF_F ? 0.f : 1.f / l;
+      float inv = lse == -CUDART_INF_F ? 0.f : __fdividef(1.f, l);
       bool use0 = s == 0, use1 = s == 1;
       if (!wk.pair) {
         sh.lse[s][row] = cnt > 0 ? lse : -CUDART_INF_F;
@@ -696,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lse = top;
         } else {
           const float e0 = ex2(l0 - top), e1 = ex2(l1 - top);
-          lse = top + log2f(e0 + e1);
+          lse = top + __log2f(e0 + e1);
           const float f = __fdividef(1.f, e0 + e1);
           w0 = e0 * f * sh.inv[0][row];
           w1 = e1 * f * sh.inv[1][row];
@@ -733,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // new tokens' infinities and NaN that this row sees
             for (int key = max(r.ctx, wk.t0 * KT); key < min(r.ctx + r.n, wk.t1 * KT); ++key) {
               const int jn = key - r.ctx;
-              if (!(mask_bits(g, mrow, i, jn) & 1)) continue;
+              if (!(mask_bits(g, mrow, first, i, jn) & 1)) continue;
               const long long col = key >> g.log2_page;
               const int pg = col < a.table_width ? a.block_table[(int64_t)wk.b * a.table_width + col] : -1;
               if (pg < 0 || pg >= a.cache.num_pages) continue;
@@ -810,7 +838,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join_kernel(const
   if (cut.parts == 0) return;
   const ft_attn_args& a = g.a;
   const int tile_rows = g.tpt * g.G;
-  for (int x = blockIdx.y * kJoinThreads + threadIdx.x; x < cut.rows * (D / 4); x += kJoinBlocks * kJoinThreads) {
+  for (int x = blockIdx.y * kJoinThreads + threadIdx.x; x < cut.rows * (D / 4); x += gridDim.y * kJoinThreads) {
     const int col = x / cut.rows, rr = x - col * cut.rows;  // rows fastest: contiguous in the parts
     const int tile = rr >= tile_rows ? 1 : 0, row = rr - tile * tile_rows;
     auto slot = [&](int p) { return (c0 + p) * 2 + (p == 0 ? 1 : 0); };
@@ -907,7 +935,10 @@ int launch(const Args& g, int grid, cudaStream_t st) {
   pdl_config(cfg, attr, dim3(grid), dim3(kThreads), C::SMEM + sizeof(Shared), st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attention_kernel<E, D>, mq, mk, mv, g);
   if (e == cudaSuccess) {
-    pdl_config(cfg, attr, dim3(grid, kJoinBlocks), dim3(kJoinThreads), 0, st);
+    // blocks for the most rows an item can have
+    const int most = std::min(a.max_tokens, 2 * g.tpt) * g.G * (D / 4);
+    const int blocks = std::min((most + kJoinThreads - 1) / kJoinThreads, kJoinBlocks);
+    pdl_config(cfg, attr, dim3(grid, blocks), dim3(kJoinThreads), 0, st);
     e = cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<E, D>, g);
   }
   if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention launch failed: %s", cudaGetErrorString(e));

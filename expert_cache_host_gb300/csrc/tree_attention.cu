@@ -825,11 +825,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the items that were cut; the blocks of a column share an
 // item.  With L_c a part's log2 sum and O_c its normalised output,
-// out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c, parts in the order of their
-// keys.  A thread takes 4 outputs of a row.  The parts are in L2.  Launched as
-// a programmatic dependent of the kernel above.
-// (kJoinBatch parts' loads are in flight at a time: the kernel is latency.)
-constexpr int kJoinThreads = 256, kJoinBlocks = 8, kJoinBatch = 8;
+// out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c.  The parts are in L2 and the
+// kernel is latency, so a batch's loads are all in flight before the first is
+// used, and where the item has few outputs several lanes share one (its parts in
+// stretches, joined in order).  A lane takes 4 outputs of a row.  Launched as a
+// programmatic dependent of the kernel above.
+constexpr int kJoinThreads = 128, kJoinBlocks = 24, kJoinBatch = 8, kJoinSplit = 4;
+
+struct Part {
+  float top, sum;  // log2 reference, sum of 2^(L_c - top)
+  float4 acc;      // sum of 2^(L_c - top) O_c
+  __device__ __forceinline__ void move(float to) {
+    const float f = top == to ? 1.f : ex2(top - to);
+    top = to;
+    sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+  }
+};
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_attention_join_kernel(const __grid_constant__ Args g) {
   pdl_wait();
@@ -837,51 +849,72 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join_kernel(const
   const Cut cut = g.cut[c0];
   if (cut.parts == 0) return;
   const ft_attn_args& a = g.a;
-  const int tile_rows = g.tpt * g.G;
-  for (int x = blockIdx.y * kJoinThreads + threadIdx.x; x < cut.rows * (D / 4); x += gridDim.y * kJoinThreads) {
+  const int tile_rows = g.tpt * g.G, outputs = cut.rows * (D / 4), warps = gridDim.y * (kJoinThreads / 32);
+  const int lane = threadIdx.x & 31, w = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  int split = 1;
+  while (split < kJoinSplit && outputs * split * 2 <= warps * 32 && split < cut.parts) split *= 2;
+  const int per = 32 / split, slice = lane / per;  // outputs of a warp; this lane's stretch of the parts
+  const int first = cut.parts * slice / split, last = cut.parts * (slice + 1) / split;
+  auto slot = [&](int p) { return (c0 + p) * 2 + (p == 0 ? 1 : 0); };
+  for (int x0 = w * per; x0 < outputs; x0 += warps * per) {
+    const int x = min(x0 + lane % per, outputs - 1);
     const int col = x / cut.rows, rr = x - col * cut.rows;  // rows fastest: contiguous in the parts
     const int tile = rr >= tile_rows ? 1 : 0, row = rr - tile * tile_rows;
-    auto slot = [&](int p) { return (c0 + p) * 2 + (p == 0 ? 1 : 0); };
-    float top = -CUDART_INF_F, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    Part q{-CUDART_INF_F, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     bool nan = false;
-    for (int p0 = 0; p0 < cut.parts; p0 += kJoinBatch) {
+    for (int p0 = first; p0 < last; p0 += kJoinBatch) {
       float l[kJoinBatch];
       float4 o[kJoinBatch];
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
-        const int at = slot(min(p0 + i, cut.parts - 1));
-        l[i] = __ldcg(&g.part_lse[at * 256 + tile * 128 + row]);
-        o[i] = __ldcg(&g.part_o[((int64_t)(at * 2 + tile) * (D / 4) + col) * 128 + row]);
+        l[i] = -CUDART_INF_F;
+        if (p0 + i < last) {
+          const int at = slot(p0 + i);
+          l[i] = __ldcg(&g.part_lse[at * 256 + tile * 128 + row]);
+          o[i] = __ldcg(&g.part_o[((int64_t)(at * 2 + tile) * (D / 4) + col) * 128 + row]);
+        }
       }
-      float most = top;
+      float most = q.top;
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
-        if (p0 + i >= cut.parts) l[i] = -CUDART_INF_F;
         nan |= l[i] != l[i];
         most = fmaxf(most, l[i]);
       }
       if (most == -CUDART_INF_F) continue;
-      const float f = ex2(top - most);
-      top = most;
-      sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+      q.move(most);
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
         const float e = ex2(l[i] - most);
         if (e > 0.f) {
-          sum += e;
-          acc.x = fmaf(e, o[i].x, acc.x), acc.y = fmaf(e, o[i].y, acc.y);
-          acc.z = fmaf(e, o[i].z, acc.z), acc.w = fmaf(e, o[i].w, acc.w);
+          q.sum += e;
+          q.acc.x = fmaf(e, o[i].x, q.acc.x), q.acc.y = fmaf(e, o[i].y, q.acc.y);
+          q.acc.z = fmaf(e, o[i].z, q.acc.z), q.acc.w = fmaf(e, o[i].w, q.acc.w);
         }
       }
     }
-    if (nan) sum = CUDART_NAN_F;  // a part's scores held NaN: the row is NaN
-    const float inv = top == -CUDART_INF_F && !nan ? 0.f : 1.f / sum;
+    // the stretches, lower parts first
+    for (int s = per; s < 32; s *= 2) {
+      Part r;
+      r.top = __shfl_down_sync(~0u, q.top, s);
+      r.sum = __shfl_down_sync(~0u, q.sum, s);
+      r.acc.x = __shfl_down_sync(~0u, q.acc.x, s), r.acc.y = __shfl_down_sync(~0u, q.acc.y, s);
+      r.acc.z = __shfl_down_sync(~0u, q.acc.z, s), r.acc.w = __shfl_down_sync(~0u, q.acc.w, s);
+      nan |= __shfl_down_sync(~0u, (int)nan, s) != 0;
+      const float most = fmaxf(q.top, r.top);
+      if (most != -CUDART_INF_F) {
+        q.move(most), r.move(most);
+        q.sum += r.sum;
+        q.acc.x += r.acc.x, q.acc.y += r.acc.y, q.acc.z += r.acc.z, q.acc.w += r.acc.w;
+      }
+    }
+    if (slice != 0 || x0 + lane >= outputs) continue;
+    if (nan) q.sum = CUDART_NAN_F;  // a part's scores held NaN: the row is NaN
+    const float inv = q.sum == 0.f ? 0.f : 1.f / q.sum;
     const int h = cut.h * g.G + row % g.G;
     const int64_t t = cut.token0 + tile * g.tpt + row / g.G;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + col * 4) =
-        make_uint2(Elem<E>::pack(acc.x * inv, acc.y * inv), Elem<E>::pack(acc.z * inv, acc.w * inv));
-    if (a.lse && col == 0) a.lse[t * a.q_heads + h] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * kLn2;
+        make_uint2(Elem<E>::pack(q.acc.x * inv, q.acc.y * inv), Elem<E>::pack(q.acc.z * inv, q.acc.w * inv));
+    if (a.lse && col == 0) a.lse[t * a.q_heads + h] = q.sum == 0.f ? -CUDART_INF_F : (q.top + log2f(q.sum)) * kLn2;
   }
 }
 
@@ -935,8 +968,8 @@ int launch(const Args& g, int grid, cudaStream_t st) {
   pdl_config(cfg, attr, dim3(grid), dim3(kThreads), C::SMEM + sizeof(Shared), st);
   cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attention_kernel<E, D>, mq, mk, mv, g);
   if (e == cudaSuccess) {
-    // blocks for the most rows an item can have
-    const int most = std::min(a.max_tokens, 2 * g.tpt) * g.G * (D / 4);
+    // blocks for the most rows an item can have, so that its outputs can be shared by kJoinSplit lanes
+    const int most = std::min(a.max_tokens, 2 * g.tpt) * g.G * (D / 4) * kJoinSplit;
     const int blocks = std::min((most + kJoinThreads - 1) / kJoinThreads, kJoinBlocks);
     pdl_config(cfg, attr, dim3(grid, blocks), dim3(kJoinThreads), 0, st);
     e = cudaLaunchKernelEx(&cfg, tree_attention_join_kernel<E, D>, g);

@@ -488,7 +488,8 @@ typedef struct ft_kv_cache {
  * tokens follow one another.  free_left must not be free_count.  Where pages
  * or columns run out, slots (and the table's columns) become -1, where rows
  * run out the last requests' new tokens are cut, and *status gets
- * FT_ST_NO_ROOM.
+ * FT_ST_NO_ROOM.  Pages past ceil(ctx_len/page_size) that an earlier step began
+ * for tokens since dropped are the caller's again (push them back).
  * Integer results, each equal to the sequential definition. */
 typedef struct ft_plan_args {
   const int32_t* ctx_len;

@@ -581,6 +581,55 @@ def test_attention_many_requests(ft):
     a.run().check()
 
 
+def gpu_reference(a):
+    """Attn.reference on the GPU in 64 bits, for long contexts."""
+    T, Hq, D, G = a.T, a.Hq, a.D, a.Hq // a.Hkv
+    out, mag = (torch.zeros((T, Hq, D), dtype=torch.float64, device="cuda") for _ in range(2))
+    lse, top = (torch.full((T, Hq), v, dtype=torch.float64, device="cuda") for v in (-math.inf, 1.0))
+    for b, (c, n) in enumerate(zip(a.ctx, a.new)):
+        if n == 0:
+            continue
+        k, v = (x[a.rows[b]].double() for x in (a.k, a.v))
+        hidden = torch.zeros((n, c + n), dtype=torch.bool, device="cuda")
+        hidden[:, c:] = torch.from_numpy(~a.seen[b]).cuda()
+        t = slice(a.start[b], a.start[b] + n)
+        for h in range(Hq):
+            s = (a.q[t, h].double() @ k[:, h // G].T * a.scale).masked_fill(hidden, -math.inf)
+            top[t, h] = s.masked_fill(hidden, 0).abs().amax(1).clamp(min=1)
+            lse[t, h] = torch.logsumexp(s, 1)
+            p = torch.softmax(s, 1)
+            out[t, h], mag[t, h] = p @ v[:, h // G], p @ v[:, h // G].abs()
+    return tuple(x.cpu().numpy() for x in (out, lse, mag, top))
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P,layout", [
+    # many tiles to a CTA, one and two row tiles side by side
+    ([21000, 300, 9000, 33000, 5], [32, 1, 17, 5, 40], 32, 4, 128, "bf16", 16, "token"),
+    ([30000, 17000, 128, 4097], [3, 50, 1, 64], 40, 8, 64, "f16", 64, "head"),
+    ([5000] * 40 + [100] * 40, [1, 20] * 40, 16, 2, 128, "f16", 128, "token")])
+def test_attention_long_contexts(ft, ctx, new, Hq, Hkv, D, dtype, P, layout):
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, layout, seed=sum(new)).run()
+    a.reference = lambda: gpu_reference(a)
+    a.check()
+    assert a.status.item() == 0
+
+
+def test_attention_back_to_back(ft):
+    """Calls of several batches one after another without a pause, each with the result it has alone."""
+    batch = [Attn(ft, [9000, 60, 3000], [20, 1, 5], 32, 4, 128, "bf16", 16, seed=20 + i) for i in range(3)]
+    want = []
+    for a in batch:
+        a.run()
+        want.append((a.out.clone(), a.lse.clone()))
+        a.out.zero_()
+    for _ in range(20):
+        for a in batch:
+            ft.ft_tree_attention(a.args, stream())
+    torch.cuda.synchronize()
+    for a, (out, lse) in zip(batch, want):
+        assert torch.equal(a.out, out) and torch.equal(a.lse, lse) and a.status.item() == 0
+
+
 # ---------------------------------------------------------------- log probabilities
 
 def run_logprob(ft, x, tokens, top):

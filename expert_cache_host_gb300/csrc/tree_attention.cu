@@ -141,7 +141,7 @@ struct Req {
 __device__ __forceinline__ Req request(const Args& g, int b) {
   Req r;
   r.q0 = g.a.q_start[b];
-  r.n = max(min(g.a.q_start[b + 1], g.a.max_tokens) - r.q0, 0);
+  r.n = r.q0 < 0 ? 0 : max(min(g.a.q_start[b + 1], g.a.max_tokens) - r.q0, 0);
   r.ctx = max(g.a.ctx_len[b], 0);
   r.tiles = (int)(((long long)r.ctx + r.n + KT - 1) / KT);
   r.blocks = (r.n + 2 * g.tpt - 1) / (2 * g.tpt);
@@ -1003,7 +1003,7 @@ extern "C" int ft_tree_attention(const ft_attn_args* args, void* stream) {
   if (!is_16b(a.q) || !is_16b(a.out) || !is_16b(a.workspace) || a.q_stride < 0 || a.out_stride < 0 || a.q_stride % 8 ||
       a.out_stride % 8)
     return record_error(FT_E_ARG, "q, out and workspace must be 16-byte aligned, row strides multiples of 8 elements");
-  if (!(a.scale - a.scale == 0.f)) return record_error(FT_E_ARG, "scale must be finite");
+  if (!(fabsf(a.scale) < 1e37f)) return record_error(FT_E_ARG, "scale must be finite (below 1e37)");
   const int grid = sm_count(), D = a.cache.head_dim;
   const uint64_t need = workspace(grid, D);
   if (a.workspace_bytes < need)

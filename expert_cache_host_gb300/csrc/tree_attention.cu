@@ -121,8 +121,10 @@ __device__ __forceinline__ Req request(const Args& g, int b) {
 // pull on HBM (D = 128, measured).
 constexpr int kPairUnits = 3, kSingleUnits = 2;
 // An item costs this much besides (its Q, the first tile's way through the
-// pipeline, its output), counted after its tiles.
-constexpr int kItemUnits = 3;
+// pipeline, its output), counted after its tiles.  24 requests of 100..8192
+// keys: 39.2 us with 6, 40.3 with 3, 46.2 with 0; 40 requests of up to 3001 keys
+// and 37 tokens, f16, D = 64: 53.1, 61.6, 68.8.
+constexpr int kItemUnits = 6;
 // Units of all but the last block, and of the last, per tile.
 __device__ __forceinline__ int last_weight(const Args& g, const Req& r) {
   return r.n - (r.blocks - 1) * 2 * g.tpt > g.tpt ? kPairUnits : kSingleUnits;

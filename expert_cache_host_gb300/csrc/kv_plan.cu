@@ -12,7 +12,9 @@
 // launch, one load of the lengths, one block-wide scan, then the parents'
 // chain.  So every CTA (256 rows) scans the requests itself, up to the last
 // one it needs, instead of reading another launch's sums: requests are a few
-// thousand at most and their lengths stay in L2.
+// thousand at most and their lengths stay in L2.  64 requests with a token each
+// take 2.6 us, 256 with 4400 drafted tokens 4.6 us (graph replay; an empty launch
+// about 1.5).
 #include "attn_side.h"
 #include "tma.h"
 

@@ -8,14 +8,17 @@
 // takes S's place as packed 16-bit pairs and is the A operand of the second
 // product from there.
 //
-// What bounds it: K and V are read once from HBM and serve 128 or 256 rows;
-// a few rows leave it HBM-bound (a 128-key tile is 64 KB at D = 128, about 3000
-// cycles of one SM's share, its two products about 1000), 256 rows and more
-// bring the products level with the reads.  So:
+// What bounds it: K and V are read once from HBM and serve 128 or 256 rows.  A
+// 128-key tile is 64 KB at D = 128, 2750 cycles of one SM's share of HBM; its two
+// products take 1031 cycles per 128 rows.  So few rows leave it HBM-bound (32
+// single tokens over 16K keys, 1.07 GB: 168 us = 6.4 TB/s) and 256 rows bring
+// the products level with the reads (32 trees of 24..32 tokens over 8K..32K
+// keys, 1.37 GB, 0.30 TFLOP: 250 us = 5.5 TB/s, 1190 TFLOP/s; a tile takes 2700
+// cycles, 1320 of them one stream's softmax beside the other's products).  So:
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same
-//    number of key tiles of the flattened list of items, whatever the lengths;
-//    an item cut over several CTAs leaves partial outputs in the workspace,
+//    amount of the flattened list of items, whatever the lengths (24 requests of
+//    100..8192 keys, 160 MB: 39 us, of which 6 the join's); an item cut over several CTAs leaves partial outputs in the workspace,
 //    which a second small kernel joins in order.
 //  - two streams of (S, softmax, O) per CTA: while the four softmax warps of
 //    one work, the tensor cores run the other's products.  With more than 128
@@ -25,8 +28,8 @@
 //    page (or per half of a head's 128 numbers), running ahead across items.
 //
 // Warps 0-3 and 4-7: softmax of stream 0 and 1 (a thread per row); warp 8: TMA;
-// warp 9: tensor-core issue; warp 10: V rows (below).  All waits
-// are bounded (FT_ST_TIMEOUT).
+// warp 9: tensor-core issue; warp 10: V rows (below).  All waits are bounded
+// (FT_ST_TIMEOUT).
 //
 // Keys a row does not see get S = -inf by selection, so their bits do not
 // matter.  For V the product would turn 0 x NaN into NaN: rows of V past the

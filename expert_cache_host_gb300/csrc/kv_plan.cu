@@ -13,8 +13,7 @@
 // chain.  So every CTA (256 rows) scans the requests itself, up to the last
 // one it needs, instead of reading another launch's sums: requests are a few
 // thousand at most and their lengths stay in L2.  64 requests with a token each
-// take 2.6 us, 256 with 4400 drafted tokens 4.6 us (graph replay; an empty launch
-// about 1.5).
+// take 2.6 us, 256 with 4400 drafted tokens 4.3 us (graph replay).
 #include "attn_side.h"
 #include "tma.h"
 
@@ -23,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 4;  // requests a thread scans at a time
+constexpr int kBehind = kThreads;  // rows before the CTA's whose parents it keeps at hand: a tree that began there
 
 // Exclusive sum over the block of each thread's v; `total` is the block's sum.
 template <typename T>
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const ft_plan_args a,
   __shared__ int sh[kThreads / 32];
   __shared__ long long shl[kThreads / 32];
   __shared__ int rec_start[kThreads], rec_req[kThreads], rec_ctx[kThreads], rec_page[kThreads], rec_n[kThreads];
-  __shared__ int s_parent[kThreads];
+  __shared__ int s_parent[kBehind + kThreads];  // of the rows from t0 - kBehind on
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int P = 1 << log2_page;
   const int t0 = blockIdx.x * kThreads, t = t0 + tid;
@@ -62,7 +62,11 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const ft_plan_args a,
   rec_req[tid] = -1;
   pdl_wait();
   pdl_trigger();
-  if (a.parents) s_parent[tid] = t < a.max_tokens ? a.parents[t] : -1;
+  if (a.parents) {
+    static_assert(kBehind == kThreads, "a row in the window and one behind it per thread");
+    s_parent[tid] = t >= kBehind ? a.parents[t - kBehind] : -1;  // (t - kBehind < t0, so it is a row)
+    s_parent[kBehind + tid] = t < a.max_tokens ? a.parents[t] : -1;
+  }
   const int free_count = *a.free_count;
   __syncthreads();
 
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const ft_plan_args a,
         }
         if (cw < a.mask_words) bits |= 1u << (cur & 31);
         const int g = start + cur;
-        int up = g >= t0 ? s_parent[g - t0] : a.parents[g];
+        int up = g >= t0 - kBehind ? s_parent[g - t0 + kBehind] : a.parents[g];
         if (up >= cur || up < -1) {
           fault |= FT_ST_BAD_TREE;
           up = -1;

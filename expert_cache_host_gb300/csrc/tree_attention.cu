@@ -679,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items_of_stream;
         tc_fence_after();
       }
-      const bool nonfinite = wk.t1 * KT > r.ctx && sh.nonfinite[item & 3];  // (written where an item has new keys)
       // Rows' output: with a row tile per stream the thread's own; else the two
       // streams' halves of the keys joined, each warpgroup half of the columns.
       float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + __log2f(l) : -CUDART_INF_F;
@@ -709,6 +708,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         c1 = c0 + D / 2;
         inv = 1.f;
       }
+      // Written where an item has new keys, before the product of their tile: without row tile pairs the other
+      // stream's warps know that it is only past the barrier above.
+      const bool nonfinite = wk.t1 * KT > r.ctx && sh.nonfinite[item & 3];
       use0 = use0 && wk.count(0) > 0;
       use1 = use1 && wk.count(1) > 0;
       const bool whole = wk.t0 == 0 && wk.t1 == r.tiles;

@@ -498,6 +498,19 @@ def test_attention_seen_nan_and_inf_reach_the_output(ft):
     assert np.isfinite(got).all()
 
 
+def test_attention_seen_inf_where_a_cta_has_both_streams(ft):
+    """Enough requests that one CTA has an item's context tile and its new tokens' tile: every column of a row that
+    sees an infinity gets it, whichever warps write the column."""
+    a = Attn(ft, [250] * 80, [4] * 80, 32, 8, 128, "bf16", 16, mask="chain", seed=15)
+    for b in range(80):
+        a.v[a.rows[b][0][251], a.rows[b][1][251]] = float("inf")  # new token 1, all heads and columns
+    for _ in range(3):
+        a.out.zero_()
+        a.run()
+        got = a.out.float().view(80, 4, 32, 128)
+        assert bool(torch.isfinite(got[:, 0]).all()) and bool(torch.isposinf(got[:, 1:]).all())
+
+
 def test_attention_strided_rows_and_shared_buffer(ft):
     """Keys and values interleaved in one buffer, q and out as slices of wider rows."""
     a = Attn(ft, [200, 5], [3, 9], 8, 2, 128, "bf16", 16, seed=9)

@@ -296,7 +296,8 @@ cudaError_t launch(Args g, cudaStream_t st) {
   const int iter = many ? 4 : 1;
   g.groups = (sets + iter - 1) / iter;
   const int64_t units = (int64_t)g.a.T * g.groups;
-  const int64_t all = (units + kWarps - 1) / kWarps, grid = many ? std::min<int64_t>(all, sm_count() * (HALVES ? kBlocks : kBlocksOther)) : all;
+  const int64_t all = (units + kWarps - 1) / kWarps, resident = sm_count() * (HALVES ? kBlocks : kBlocksOther);
+  const int64_t grid = many ? std::min(all, resident) : all;
   if (units > 0x7FFFFF00) return cudaErrorInvalidValue;  // (refused before: T is limited)
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
@@ -338,6 +339,9 @@ extern "C" int ft_qk_norm_rope(const ft_qk_args* args, void* stream) {
   if (a.rot_dim % 16) return record_error(FT_E_UNSUPPORTED, "rot_dim must be a multiple of 16");
   if (!is_16b(a.cos_sin) || !is_16b(a.q_weight) || !is_16b(a.k_weight))
     return record_error(FT_E_ARG, "cos_sin and the weights must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+       reinterpret_cast<uintptr_t>(a.q_out)) % 2)
+    return record_error(FT_E_ARG, "q, k, v and q_out must be aligned to their type");
   if (!(a.eps >= 0.f)) return record_error(FT_E_ARG, "eps must not be negative");
   if (a.q_out == a.q && a.q_out_stride != a.q_stride)
     return record_error(FT_E_ARG, "q_out on top of q needs the same stride");

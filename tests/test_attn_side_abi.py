@@ -98,6 +98,11 @@ def test_qk_refusals(kw, code):
     refused(ft.ft_qk_norm_rope, qk(**kw), code)
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v", "q_out"])
+def test_qk_refuses_rows_between_elements(name):
+    refused(ft.ft_qk_norm_rope, qk(**{name: PTR + 1}), ft.FT_E_ARG)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(max_tokens=-1), ft.FT_E_ARG), (dict(num_reqs=-1), ft.FT_E_ARG), (dict(q_heads=0), ft.FT_E_ARG),
     (dict(q_heads=7), ft.FT_E_ARG), (dict(q_heads=2 * 129), ft.FT_E_UNSUPPORTED), (dict(q=0), ft.FT_E_ARG),

@@ -18,8 +18,9 @@
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same
 //    amount of the flattened list of items, whatever the lengths (24 requests of
-//    100..8192 keys, 160 MB: 39 us, of which 6 the join's); an item cut over several CTAs leaves partial outputs in the workspace,
-//    which a second small kernel joins in order.
+//    100..8192 keys, 160 MB: 39 us, of which 6 the join's); an item cut over
+//    several CTAs leaves partial outputs in the workspace, which a second small
+//    kernel joins in order.
 //  - two streams of (S, softmax, O) per CTA: while the four softmax warps of
 //    one work, the tensor cores run the other's products.  With more than 128
 //    rows the streams are the two row tiles and share every K and V tile; with
@@ -82,7 +83,7 @@ struct Args {
 
 // An item cut over several CTAs: parts = 0 where there is none.
 struct Cut {
-  int parts, rows, token0, h, pad[4];
+  int parts, rows, token0, h;
 };
 
 __host__ __device__ constexpr size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256; }
@@ -106,28 +107,35 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Requests' sizes and the walk over this CTA's work.
-struct Req {
-  int q0, n, ctx, tiles, blocks;
-};
-__device__ __forceinline__ Req request(const Args& g, int b) {
-  Req r;
-  r.q0 = g.a.q_start[b];
-  r.n = r.q0 < 0 ? 0 : max(min(g.a.q_start[b + 1], g.a.max_tokens) - r.q0, 0);
-  r.ctx = max(g.a.ctx_len[b], 0);
-  r.tiles = (int)(((long long)r.ctx + r.n + KT - 1) / KT);
-  r.blocks = (r.n + 2 * g.tpt - 1) / (2 * g.tpt);
-  return r;
-}
 // A tile costs a CTA this many units: with two row tiles the products and both
-// streams' softmax take 3400 cycles, with one 1750 alone and 2800 when all SMs
-// pull on HBM (D = 128, measured).
+// streams' softmax take 2700 cycles, with one 1750 (D = 128, measured).
 constexpr int kPairUnits = 3, kSingleUnits = 2;
 // An item costs this much besides (its Q, the first tile's way through the
 // pipeline, its output), counted after its tiles.  24 requests of 100..8192
 // keys: 39.2 us with 6, 40.3 with 3, 46.2 with 0; 40 requests of up to 3001 keys
 // and 37 tokens, f16, D = 64: 53.1, 61.6, 68.8.
 constexpr int kItemUnits = 6;
+// Requests' sizes and the walk over this CTA's work.
+struct Req {
+  int q0, n, ctx, tiles, blocks;
+};
+// Beyond this many keys a tile's end would not fit 31 bits.
+constexpr uint32_t kMostKeys = 0x7FFFFFFFu - 2 * KT;
+__device__ __forceinline__ Req request(const Args& g, int b) {
+  Req r;
+  r.q0 = g.a.q_start[b];
+  r.n = r.q0 < 0 ? 0 : max(min(g.a.q_start[b + 1], g.a.max_tokens) - r.q0, 0);
+  r.ctx = max(g.a.ctx_len[b], 0);
+  const uint32_t keys = (uint32_t)r.ctx + r.n;
+  r.tiles = (int)((keys + KT - 1) / KT);
+  r.blocks = (r.n + 2 * g.tpt - 1) / (2 * g.tpt);
+  // (a head's units must fit 31 bits too)
+  if (keys > kMostKeys || __umulhi((uint32_t)(r.tiles * kPairUnits + kItemUnits), 2u * r.blocks) != 0) {
+    if (g.a.status) atomicOr(g.a.status, FT_ST_BAD_SLOT);
+    r.n = r.tiles = r.blocks = 0;
+  }
+  return r;
+}
 // Units of all but the last block, and of the last, per tile.
 __device__ __forceinline__ int last_weight(const Args& g, const Req& r) {
   return r.n - (r.blocks - 1) * 2 * g.tpt > g.tpt ? kPairUnits : kSingleUnits;
@@ -280,7 +288,7 @@ __device__ __forceinline__ uint32_t fix_v(uint8_t* v, int lane, int row_shift, u
       const uint32_t y = (e[k] & x) ^ x;
       all |= (y - 0x00010001u) & ~y & 0x80008000u;
     }
-    if (all) {  // (a borrow can also raise the flag: looked at exactly here)
+    if (all) {  // (a borrow from the lower half can raise the upper's flag: looked at exactly here)
       bool bad = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -343,8 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       lo = deal.first(c);
       return c >= deal.grid ? 0 : c == deal.grid - 1 ? (int)min(total - lo, 0x7FFFFFFFll) : deal.per + (c < deal.extra);
     };
-    // The walk's start, `at` units into request b.  (A request of more than 2^32
-    // units does not occur: 2^31 keys are 2^24 tiles.)
+    // The walk's start, `at` units into request b.
     auto place = [&](Walk& w, const Req& r, int b, uint32_t at) {
       const uint32_t per_head = (uint32_t)head_units(g, r), per_block = (uint32_t)r.tiles * kPairUnits + kItemUnits;
       w.b = b;

@@ -560,6 +560,9 @@ int ft_qk_norm_rope(const ft_qk_args* args, void* stream);
  *   lse[t, h] = ln sum_j exp(scale * q.k_j)        (float32, may be NULL)
  * A row that sees no key gives 0 and -inf.  Keys a row does not see take no
  * part, whatever their bits; cache rows past a request's keys are never used.
+ * Pages that are missing (outside the cache or past the table) hold no keys and
+ * are reported (FT_ST_BAD_SLOT), and so is a request of more than 2^31 - 257
+ * keys, whose rows are not written.
  * Rows at or past q_start[num_reqs] are not written.  Scores, the softmax's
  * maximum and sum and the output's sum are held in 32 bits; the
  * probabilities are rounded to the cache's type for the second product.

@@ -543,6 +543,23 @@ def test_attention_bad_pages_are_reported_and_absent(ft):
     a.check()
 
 
+@pytest.mark.parametrize("ctx", [(1 << 31) - 1, (1 << 31) - 256])
+def test_attention_request_of_too_many_keys_is_reported_and_left(ft, ctx):
+    a = Attn(ft, [100, 20, 300], [4, 3, 5], 8, 2, 128, "bf16", 16, mask="chain", seed=16)
+    a.d_ctx[1] = ctx
+    a.run()
+    assert a.status.item() == ft.FT_ST_BAD_SLOT
+    assert bool((a.out[4:7] == 5).all()) and bool((a.lse[4:7] == 5).all())
+    got, lse = a.out.clone(), a.lse.clone()
+    a.d_ctx[1] = 20
+    a.status.zero_()
+    a.run()
+    a.check()
+    for rows in (slice(0, 4), slice(7, 12)):  # split elsewhere, so close and not the same
+        assert bool(torch.allclose(got[rows].float(), a.out[rows].float(), atol=2.0 ** -6, rtol=2.0 ** -6))
+        assert bool(torch.allclose(lse[rows], a.lse[rows], atol=1e-3))
+
+
 def test_attention_rows_past_the_last_request_stay(ft):
     a = Attn(ft, [60, 10], [3, 2], 4, 1, 64, "f16", 16, seed=11)
     a.d_start[2] = 4  # the second request's last token is not part of the step

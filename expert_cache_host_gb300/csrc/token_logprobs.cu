@@ -11,8 +11,9 @@
 // logits are clamped and their maximum taken in packed pairs, the rest runs on
 // packed fp32 pairs, so that an element is 1 exponential and 3.5 other
 // instructions (4000 rows of 131072 bf16 without alternatives: 6.7 TB/s, the
-// copy rate; 1024 rows with 8 alternatives 55 us, without 47).  A batch is kVecs 16-byte vectors a thread: one maximum and
-// one rescaling serve it, and the next batch's loads are in flight meanwhile.
+// copy rate; 1024 rows with 8 alternatives 55 us, without 47).  A batch is
+// kVecs 16-byte vectors a thread: one maximum and one rescaling serve it, and
+// the next batch's loads are in flight meanwhile.
 // A batch that holds NaN, or whose maximum lies near the type's ends, is done
 // again with care.
 //
@@ -20,7 +21,8 @@
 // largest value.  The top_n-th largest over groups of threads is a bound that
 // at least top_n entries reach, and only threads whose largest reaches it hold
 // such entries: a warp looks at each such thread's entries again (from L2) and
-// collects those that reach the bound, top_n and a few more.  They are ordered by a 64-bit key (value, then lower id).  Where they overflow the list
+// collects those that reach the bound, top_n and a few more.  They are ordered
+// by a 64-bit key (value, then lower id).  Where they overflow the list
 // (thousands of equal logits) the warps walk all entries, each merging what
 // beats its own top_n-th.
 //
@@ -47,7 +49,6 @@ constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kHuge = 1e37f;  // up to here m log2(e) is far from overflow
-
 
 // Larger value, or the lower id among equals, is the larger key; 0 is below every entry.
 __device__ __forceinline__ uint64_t make_key(float v, uint32_t id) {

@@ -5,7 +5,8 @@
 //   S = sum 2^t,   U = sum t 2^t:
 //   ln sum e^x = m + ln 2 log2 S,   entropy = ln 2 (log2 S - U / S),
 // and when t falls by d for a larger m, U <- (U - d S) 2^-d, S <- S 2^-d.  (M is
-// rounded; t at x = m is that rounding, and the result takes it out again.)
+// rounded; t at x = m is that rounding, and the result takes it out again.  Past
+// |m| = 2^24, where it would pass 1, t is (x - m) log2(e).)
 //
 // HBM bounds many rows, if a batch of logits costs few instructions: 16-bit
 // logits are clamped and their maximum taken in packed pairs, the rest runs on
@@ -14,8 +15,8 @@
 // copy rate; 1024 rows with 8 alternatives 55 us, without 47).  A batch is
 // kVecs 16-byte vectors a thread: one maximum and one rescaling serve it, and
 // the next batch's loads are in flight meanwhile.
-// A batch that holds NaN, or whose maximum lies near the type's ends, is done
-// again with care.
+// A batch that holds NaN, or whose maximum lies past 2^24 or near the type's
+// lowest value, is done again with care.
 //
 // Alternatives without a second pass over HBM: each thread keeps only its
 // largest value.  The top_n-th largest over groups of threads is a bound that
@@ -48,7 +49,7 @@ constexpr int kList = 1024;  // entries that reach the bound
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kHuge = 1e37f;  // up to here m log2(e) is far from overflow
+constexpr float kNear = 16777216.f;  // up to here the rounding of m log2(e) is below 1
 
 // Larger value, or the lower id among equals, is the larger key; 0 is below every entry.
 __device__ __forceinline__ uint64_t make_key(float v, uint32_t id) {
@@ -100,14 +101,14 @@ __device__ __forceinline__ void block_merge(T (*list)[kMaxTop], int n, int w, in
 struct Sums {
   float m, s, u;  // reference, sum of 2^t, sum of t 2^t
 };
-__device__ __forceinline__ bool near(float m) { return fabsf(m) < kHuge; }
-// How far t falls when the reference moves from a to b >= a.
-__device__ __forceinline__ float fall(float a, float b) {
-  const float d = near(a) && near(b) ? __fmul_rn(a, kLog2e) - __fmul_rn(b, kLog2e) : (a - b) * kLog2e;
-  return fmaxf(d, -1e30f);  // (also for -inf - -inf)
-}
+__device__ __forceinline__ bool near(float m) { return fabsf(m) <= kNear; }
 // t of the reference itself: the rounding of M.
 __device__ __forceinline__ float rest(float m) { return near(m) ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.f; }
+// How far t falls when the reference moves from a to b >= a.
+__device__ __forceinline__ float fall(float a, float b) {
+  const float d = near(a) && near(b) ? __fmul_rn(a, kLog2e) - __fmul_rn(b, kLog2e) : (a - b) * kLog2e + (rest(b) - rest(a));
+  return fmaxf(d, -1e30f);  // (also for -inf - -inf)
+}
 __device__ __forceinline__ Sums moved(Sums a, float m) {
   const float d = fall(a.m, m), e = ex2(d);
   // d 2^d -> 0 as d -> -inf: a part that vanishes adds nothing
@@ -134,7 +135,7 @@ struct Logit;  // 16 bytes of logits
 template <>
 struct Logit<float> {
   static constexpr int N = 4;
-  static constexpr float kLow = -1e29f;
+  static constexpr float kLow = -kNear;
   static __device__ __forceinline__ void unpack(uint4 w, float* x) {
     x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
   }
@@ -187,7 +188,7 @@ struct Logit16 {
 template <>
 struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16, __nv_bfloat162> {
   static constexpr uint32_t kClamp = 0xF149F149u;  // about -1e30
-  static constexpr float kLow = -1e29f;
+  static constexpr float kLow = -kNear;
   static __device__ __forceinline__ float scalar(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 };
 template <>
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
     }
     const float2 s = split2(add2(s2[0], s2[1])), u = split2(add2(u2[0], u2[1]));
     const float bs = s.x + s.y;
-    if (bs == bs && q.m >= L::kLow && q.m < kHuge) {
+    if (bs == bs && q.m >= L::kLow && q.m <= kNear) {
       q.s += bs;
       q.u += u.x + u.y;
     } else {

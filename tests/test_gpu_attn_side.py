@@ -742,6 +742,18 @@ def test_logprobs_unusual_rows(ft, kind, dtype):
         assert (got["entropy"] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,base,step", [
+    ("f32", 0.0, 1e30), ("bf16", 0.0, 1e30), ("f32", 1e9, 64.0), ("f32", -1e9, 64.0), ("f32", 16777216.0, 2.0),
+    ("f32", -16777216.0, 2.0), ("f32", 16777216.0, 1e5), ("bf16", 3e9, 1e7), ("bf16", -3e9, 1e7), ("f32", 1e7, 1.0),
+    ("bf16", 16777216.0, 65536.0), ("f32", -1e29, 1e22), ("bf16", -2e30, 1e28)])
+def test_logprobs_far_from_zero(ft, dtype, base, step):
+    """Rows whose values are large beside their differences, on either side of 2^24 too."""
+    for T, V in ((3, 20011), (2, 70001), (400, 300)):
+        g = torch.Generator(device="cuda").manual_seed(V)
+        x = (base + torch.randn((T, V), generator=g, device="cuda", dtype=torch.float64) * step).to(DT[dtype])
+        assert check_logprob(ft, x, 5)["status"][0] == 0
+
+
 def test_logprobs_nan_inf_and_bad_tokens(ft):
     g = torch.Generator(device="cuda").manual_seed(3)
     x = torch.randn((6, 5003), generator=g, device="cuda").to(torch.bfloat16)

@@ -61,6 +61,9 @@ constexpr int kProducer = 8, kIssuer = 9, kFixer = 10;  // warps
 // The running maximum may lag behind by this much (in log2 units) before O is
 // rescaled: p <= 2^8 stays exact in fp32 sums and in range of f16.
 constexpr float kLag = 8.f;
+// The exponents c x - fl(c m) hold the rounding of c m, at most 2^-4 up to here;
+// past it (c m of 2^29 would overflow f16) they are c (x - m).
+constexpr float kFar = 1048576.f;
 
 template <int D>
 struct Cfg {
@@ -607,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int cnt = wk.count(s);
       float m = -CUDART_INF_F, l = 0.f;
+      bool far = false;  // a row's m is past kFar
       for (int j = 0; j < cnt; ++j, ++tiles_done) {
         if (!mbar_wait(&sh.s_full[s], tiles_done & 1, late)) late = true;
         tc_fence_after();
@@ -651,8 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             l *= f;
             if (grow) m = top;
+            far = __any_sync(~0u, fabsf(m) * g.c > kFar && m != -CUDART_INF_F);
           }
-          const float ref = m == -CUDART_INF_F ? 0.f : m * g.c;
+          float ref = m == -CUDART_INF_F ? 0.f : m * g.c;
+          if (far) {
+            const float from = ref == 0.f ? 0.f : m;
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] -= from;
+            ref = 0.f;
+          }
           const uint64_t c2 = pair2(g.c, g.c), ref2 = pair2(-ref, -ref);
           uint64_t sum[4] = {};
 #pragma unroll

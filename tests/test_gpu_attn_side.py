@@ -463,6 +463,34 @@ def test_attention_growing_scores(ft):
     a.run().check()
 
 
+@pytest.mark.parametrize("dtype,size,scale", [("f16", 8000.0, 0.25), ("bf16", 1e6, None), ("bf16", 1e15, None),
+                                              ("bf16", 1e6, -0.1), ("f16", 1000.0, None), ("bf16", 3000.0, -0.1)])
+def test_attention_scores_far_from_zero(ft, dtype, size, scale):
+    """Scores of 1e6 to 1e31: the row is its largest score's value wherever that stands clear of the scores' fp32 sums."""
+    ctx, new = [700, 33, 0], [3, 20, 5]
+    a = Attn(ft, ctx, new, 8, 2, 128, dtype, 16, mask="chain", seed=17, scale=scale)
+    a.q.mul_(size)
+    a.k.mul_(size)
+    a.run()
+    got, lse = a.out.double().cpu().numpy(), a.lse.double().cpu().numpy()
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+    q, clear = a.q.double().cpu().numpy(), 0
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        k, v = (x[a.rows[b]].double().cpu().numpy() for x in (a.k, a.v))
+        for i in range(n):
+            for h in range(8):
+                kk, t = k[:c + i + 1, h // 4], a.start[b] + i
+                s = kk @ q[t, h] * a.scale
+                err = 2.0 ** -17 * np.max(np.abs(kk) @ np.abs(q[t, h])) * abs(a.scale)  # 128 fp32 sums
+                first, second = s.argmax(), np.sort(s)[-2] if len(s) > 1 else -np.inf
+                assert abs(lse[t, h] - s.max()) <= err + 10
+                if s.max() - second > 2 * err + 40:
+                    clear += 1
+                    want = v[first, h // 4]
+                    assert (np.abs(got[t, h] - want) <= 2 * U[dtype] * np.abs(want) + 2.0 ** -16).all()
+    assert clear > 8 * 28 // 2
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min])
 def test_attention_unseen_keys_take_no_part(ft, value):
     """Unusual numbers in new keys and values that a row does not see (other branches of its tree) and past the

@@ -106,19 +106,27 @@ __device__ __forceinline__ bool near(float m) { return fabsf(m) <= kNear; }
 __device__ __forceinline__ float rest(float m) { return near(m) ? fmaf(m, kLog2e, -__fmul_rn(m, kLog2e)) : 0.f; }
 // How far t falls when the reference moves from a to b >= a.
 __device__ __forceinline__ float fall(float a, float b) {
-  const float d = near(a) && near(b) ? __fmul_rn(a, kLog2e) - __fmul_rn(b, kLog2e) : (a - b) * kLog2e + (rest(b) - rest(a));
-  return fmaxf(d, -1e30f);  // (also for -inf - -inf)
+  if (__builtin_expect(near(a) && near(b), 1)) return __fmul_rn(a, kLog2e) - __fmul_rn(b, kLog2e);
+  return fmaxf((a - b) * kLog2e + (rest(b) - rest(a)), -1e30f);  // (also for -inf - -inf)
 }
 __device__ __forceinline__ Sums moved(Sums a, float m) {
   const float d = fall(a.m, m), e = ex2(d);
   // d 2^d -> 0 as d -> -inf: a part that vanishes adds nothing
   return Sums{m, a.s * e, e > 0.f ? fmaf(d, a.s, a.u) * e : 0.f};
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -CUDART_INF_F) return a;
-  const Sums x = moved(a, m), y = moved(b, m);
-  return Sums{m, x.s + y.s, x.u + y.u};
+// The sum of each N neighbouring lanes' parts, in a fixed order: to their maximum, then added.
+template <int N>
+__device__ __forceinline__ Sums lanes_sum(Sums q) {
+  float m = q.m;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  if (m != -CUDART_INF_F) q = moved(q, m);
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    q.s += __shfl_xor_sync(~0u, q.s, o);
+    q.u += __shfl_xor_sync(~0u, q.u, o);
+  }
+  return q;
 }
 // One entry with care: any value.
 __device__ __forceinline__ void add_entry(Sums& q, float x) {
@@ -307,19 +315,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
       add_entry(q, x);
     }
   }
-  // the block's sums, in a fixed order: to the warp's maximum, then added
-  {
-    float m = q.m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    if (m != -CUDART_INF_F) q = moved(q, m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      q.s += __shfl_xor_sync(~0u, q.s, o);
-      q.u += __shfl_xor_sync(~0u, q.u, o);
-    }
-    if (lane == 0) sh.warp_sums[w] = q;
-  }
+  q = lanes_sum<32>(q);
+  if (lane == 0) sh.warp_sums[w] = q;
   if (__any_sync(~0u, nan) && lane == 0) sh.nan = 1;  // (read after the barriers below)
 
   if (a.top_n > 0) {
@@ -397,9 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   }
   // this CTA's sums and list, into the first CTA's shared memory
   if (w == 0) {
-    Sums s = sh.warp_sums[lane % kWarps];
-#pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) s = join(s, Sums{__shfl_xor_sync(~0u, s.m, o), __shfl_xor_sync(~0u, s.s, o), __shfl_xor_sync(~0u, s.u, o)});
+    const Sums s = lanes_sum<kWarps>(sh.warp_sums[lane % kWarps]);
     RowShared* to = &sh;
     if constexpr (CS > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
@@ -421,13 +416,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   if (rank != 0) return;
   if (CS > 1 && a.top_n > 0) block_merge(sh.from, CS, w, lane);
   if (w == 0) {
-    Sums s = sh.from_sums[0];
-    int any_nan = sh.from_nan[0];
-#pragma unroll
-    for (int r = 1; r < CS; ++r) {
-      s = join(s, sh.from_sums[r]);
-      any_nan |= sh.from_nan[r];
-    }
+    const Sums s = lanes_sum<CS>(sh.from_sums[lane % CS]);
+    const bool any_nan = __any_sync(~0u, sh.from_nan[lane % CS] != 0);
     const bool empty = s.m == -CUDART_INF_F, inf = s.m == CUDART_INF_F;
     const float log2s = log2f(s.s);
     const float off = kLn2 * (log2s - rest(s.m));  // ln p of an entry x: x - m - off

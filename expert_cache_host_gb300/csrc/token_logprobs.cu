@@ -12,7 +12,7 @@
 // logits are clamped and their maximum taken in packed pairs, the rest runs on
 // packed fp32 pairs, so that an element is 1 exponential and 3.5 other
 // instructions (4000 rows of 131072 bf16 without alternatives: 6.7 TB/s, the
-// copy rate; 1024 rows with 8 alternatives 55 us, without 47).  A batch is
+// copy rate; 1024 rows with 8 alternatives 54 us, without 47).  A batch is
 // kVecs 16-byte vectors a thread: one maximum and one rescaling serve it, and
 // the next batch's loads are in flight meanwhile.
 // A batch that holds NaN, or whose maximum lies past 2^24 or near the type's

@@ -18,7 +18,7 @@
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same
 //    amount of the flattened list of items, whatever the lengths (24 requests of
-//    100..8192 keys, 160 MB: 39 us, of which 6 the join's); an item cut over
+//    100..8192 keys, 160 MB: 40 us, of which 6 the join's); an item cut over
 //    several CTAs leaves partial outputs in the workspace, which a second small
 //    kernel joins in order.
 //  - two streams of (S, softmax, O) per CTA: while the four softmax warps of

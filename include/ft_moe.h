@@ -521,7 +521,7 @@ int ft_kv_plan(const ft_plan_args* args, void* stream);
  *   (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i),
  * a, b = i, i + rot_dim/2, or 2i, 2i+1 where interleaved != 0.  Queries go to
  * q_out, keys to cache.k at slots[t], values unchanged to cache.v.  All in 32
- * bits, rounded once.  Heads are contiguous in a row, rows `*_stride` elements
+ * bits (a head whose sum of squares passes their range gives 0), rounded once.  Heads are contiguous in a row, rows `*_stride` elements
  * apart (any stride; 16-byte multiples run faster).  q_out may be q (same
  * stride).  A negative slot writes no key and value; a slot past the cache is
  * reported (FT_ST_BAD_SLOT) and writes none; a position outside [0, max_pos)

@@ -215,7 +215,8 @@ struct RowShared {
   float best[64];          // largest of each 4 threads
   uint8_t who[kThreads];   // threads whose largest reaches the bound
   Sums warp_sums[kWarps];
-  int n_who, count, nan;
+  int warp_nan[kWarps];    // the warp met a NaN
+  int n_who, count;
 };
 
 template <typename E, int CS>
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   const int rank = CS == 1 ? 0 : (int)(blockIdx.x % CS);
   const int t = blockIdx.x / CS;
   const E* row = static_cast<const E*>(a.logits) + (int64_t)t * a.row_stride;
-  if (tid == 0) sh.n_who = sh.count = sh.nan = 0;
+  if (tid == 0) sh.n_who = sh.count = 0;  // (used after the barrier that follows the bound)
   if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for before remote writes
 
   // The given token's logit, on its way while the row is read.
@@ -316,8 +317,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
     }
   }
   q = lanes_sum<32>(q);
-  if (lane == 0) sh.warp_sums[w] = q;
-  if (__any_sync(~0u, nan) && lane == 0) sh.nan = 1;  // (read after the barriers below)
+  nan = __any_sync(~0u, nan);
+  if (lane == 0) {
+    sh.warp_sums[w] = q;
+    sh.warp_nan[w] = nan;
+  }
 
   if (a.top_n > 0) {
     // The bound: the top_n-th largest of 64 groups of 4 threads, or 32 of 8 where
@@ -395,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   // this CTA's sums and list, into the first CTA's shared memory
   if (w == 0) {
     const Sums s = lanes_sum<kWarps>(sh.warp_sums[lane % kWarps]);
+    const bool any_nan = __any_sync(~0u, sh.warp_nan[lane % kWarps] != 0);
     RowShared* to = &sh;
     if constexpr (CS > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster has started
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
     if (a.top_n > 0) to->from[rank][lane] = sh.list[0][lane];
     if (lane == 0) {
       to->from_sums[rank] = s;
-      to->from_nan[rank] = sh.nan;
+      to->from_nan[rank] = any_nan;
     }
   } else if constexpr (CS > 1) {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");

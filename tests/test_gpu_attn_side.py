@@ -812,3 +812,23 @@ def test_logprobs_optional_outputs_and_offsets_past_32_bits(ft):
                                               V=3000, top_n=0), stream())
     torch.cuda.synchronize()
     close(ent.cpu().numpy(), logprob_reference(x, [0, 0], 0)[1])
+
+
+@pytest.mark.parametrize("T,V", [(1, 131072), (40, 30011), (400, 20000), (3, 700)])
+@pytest.mark.parametrize("top", [0, 5])
+def test_logprobs_nan_is_reported_wherever_it_lies(ft, T, V, top):
+    """One NaN in one row, at places that fall to every warp of every CTA of a row, and in the ragged ends."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((T, V + 3), generator=g, device="cuda").to(torch.bfloat16)[:, 1:V + 1]  # not on 16 bytes
+    logprob, tok, ids = torch.zeros(T, device="cuda"), dev([0] * T), dev([0] * (T * 5))
+    lps = torch.zeros(T * 5, device="cuda")
+    places = sorted({0, 6, 7, V - 1, V // 2} | set(range(100, V, max(256, V // 40 // 8 * 8 + 8))))
+    status = dev([0] * len(places))
+    for i, p in enumerate(places):
+        x[i % T, p] = float("nan")
+        ft.ft_token_logprobs(ft.make_logprob_args(logits=at(x), tokens=at(tok), logprob=at(logprob), top_ids=at(ids),
+                                                  top_logprobs=at(lps), status=at(status) + 4 * i, row_stride=x.stride(0),
+                                                  dtype=ft.FT_DTYPE_BF16, T=T, V=V, top_n=top), stream())
+        x[i % T, p] = 0
+    torch.cuda.synchronize()
+    assert status.tolist() == [ft.FT_ST_NAN] * len(places)

@@ -4,7 +4,7 @@
 // With n_b the new tokens of request b, everything a row needs is its request
 // (the last b with q_start[b] = sum_{b' < b} n_b' at or before the row) and how
 // many fresh pages the requests before it take,
-// sum_{b' < b} ceil((ctx+n)/P) - ceil(ctx/P).  A page is fresh exactly when the
+// sum_{b' < b} ceil((ctx+n)/P) - ceil(ctx/P), columns of the table only.  A page is fresh exactly when the
 // step writes its first row, so the row with (ctx + i) % P == 0 fills the
 // block-table column and no row waits for another's write.
 //
@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(kThreads) kv_plan_kernel(const ft_plan_args a,
         start[i] = min(start[i], (long long)a.max_tokens);
         n[i] = a.max_tokens - (int)start[i];
       }
-      fresh[i] = ((ctx[i] + n[i] + P - 1) >> log2_page) - ((ctx[i] + P - 1) >> log2_page);
+      // (a column past the table takes no page: nothing would hold its id)
+      fresh[i] = min((ctx[i] + n[i] + P - 1) >> log2_page, a.table_width) -
+                 min((ctx[i] + P - 1) >> log2_page, a.table_width);
       psum += fresh[i];
     }
     int ptotal;

@@ -486,9 +486,9 @@ typedef struct ft_kv_cache {
  * parents [max_tokens]: the request-local index of each row's parent, -1 for a
  * child of the context, always less than the row's own index; NULL where new
  * tokens follow one another.  free_left must not be free_count.  Where pages
- * or columns run out, slots (and the table's columns) become -1, where rows
- * run out the last requests' new tokens are cut, and *status gets
- * FT_ST_NO_ROOM.  Pages past ceil(ctx_len/page_size) that an earlier step began
+ * or columns run out, slots (and the table's columns) become -1 (a column past
+ * the table takes no page), where rows run out the last requests' new tokens
+ * are cut, and *status gets FT_ST_NO_ROOM.  Pages past ceil(ctx_len/page_size) that an earlier step began
  * for tokens since dropped are the caller's again (push them back).
  * Integer results, each equal to the sequential definition. */
 typedef struct ft_plan_args {

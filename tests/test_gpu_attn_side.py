@@ -832,3 +832,21 @@ def test_logprobs_nan_is_reported_wherever_it_lies(ft, T, V, top):
         x[i % T, p] = 0
     torch.cuda.synchronize()
     assert status.tolist() == [ft.FT_ST_NAN] * len(places)
+
+
+def test_plan_columns_past_the_table_take_no_page(ft):
+    """A request longer than its row of the table takes pages for the columns there are; the others keep theirs."""
+    P = 16
+    table = np.array([[0, 1, 2], [-1, -1, -1]], dtype=np.int32)
+    r = run_plan(ft, [40, 0], [20, 5], None, [3, 4], table, P, 25)
+    assert r["status"][0] == ft.FT_ST_NO_ROOM and r["left"][0] == 1
+    assert r["table"].tolist() == [[0, 1, 2], [4, -1, -1]]
+    assert r["slots"].tolist() == [2 * 16 + 8 + i for i in range(8)] + [-1] * 12 + [4 * 16 + i for i in range(5)]
+    # the overrun begins a page of the table, then two past it; a context that is itself past the table
+    table = np.array([[7, -1], [8, 9], [-1, -1]], dtype=np.int32)
+    r = run_plan(ft, [10, 70, 3], [50, 30, 14], None, [1, 2, 3, 4], np.concatenate([table[:2], [[5, -1]]]).astype(np.int32),
+                 P, 100)
+    assert r["status"][0] == ft.FT_ST_NO_ROOM and r["left"][0] == 2
+    assert r["table"].tolist() == [[7, 4], [8, 9], [5, 3]]
+    assert r["slots"].tolist() == [7 * 16 + 10 + i for i in range(6)] + [4 * 16 + i for i in range(16)] + [-1] * 28 + \
+        [-1] * 30 + [5 * 16 + 3 + i for i in range(13)] + [3 * 16] + [-1] * 6

@@ -4,7 +4,7 @@
 // For one request and key head, the rows that read the same keys are the
 // step's tokens times the query heads of the group (r = token * G + head).  A
 // tile is 128 rows x 128 keys: S = Q K^T, p = 2^(c S - m) with the running row
-// maximum m (c = scale log2 e), O += P V.  S, P and O live in tensor memory; P
+// maximum m (c = scale log2 e; f16 holds p times 2^11), O += P V.  S, P and O live in tensor memory; P
 // takes S's place as packed 16-bit pairs and is the A operand of the second
 // product from there.
 //
@@ -58,9 +58,23 @@ constexpr int kThreads = 384;  // 8 softmax warps, TMA, issue, V fixer, one that
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "the split must fit the launch's registers");
 constexpr int kProducer = 8, kIssuer = 9, kFixer = 10;  // warps
-// The running maximum may lag behind by this much (in log2 units) before O is
-// rescaled: p <= 2^8 stays exact in fp32 sums and in range of f16.
-constexpr float kLag = 8.f;
+// The running maximum m may lag behind by kLag (in log2 units) before O is
+// rescaled, and probabilities are held times 2^kUp, p = 2^(c S - m + kUp), so
+// that p <= 2^(kLag + kUp).  bf16 has fp32's range.  f16 has a fixed spacing of
+// 2^-24 below 2^-14, so its probabilities take the range up to 2^15: those of
+// 2^-25 of a row's largest still have all their bits, and 2^-36 is the least
+// that is not lost.  (Held as p <= 1, keys of 2^-25 each beside one large score
+// vanished from the output: half of it over 16K keys.)
+template <typename E>
+struct Held;
+template <>
+struct Held<__nv_bfloat16> {
+  static constexpr float kLag = 8.f, kUp = 0.f;
+};
+template <>
+struct Held<__half> {
+  static constexpr float kLag = 4.f, kUp = 11.f;
+};
 // The exponents c x - fl(c m) hold the rounding of c m, at most 2^-4 up to here;
 // past it (c m of 2^29 would overflow f16) they are c (x - m).
 constexpr float kFar = 1048576.f;
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 4; c < 124; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
           const float top = max3(max3(mx[0], mx[1], x[124]), max3(mx[2], mx[3], x[125]), fmaxf(x[126], x[127]));
-          const bool grow = (top - m) * g.c > kLag || m == -CUDART_INF_F;  // also the first tile with a key
+          const bool grow = (top - m) * g.c > Held<E>::kLag || m == -CUDART_INF_F;  // also the first tile with a key
           if (__any_sync(~0u, grow)) {
             const float f = grow ? (top == -CUDART_INF_F ? 1.f : ex2((m - top) * g.c)) : 1.f;
             if (j > 0) {
@@ -664,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 128; ++c) x[c] -= from;
             ref = 0.f;
           }
-          const uint64_t c2 = pair2(g.c, g.c), ref2 = pair2(-ref, -ref);
+          const uint64_t c2 = pair2(g.c, g.c), ref2 = pair2(Held<E>::kUp - ref, Held<E>::kUp - ref);
           uint64_t sum[4] = {};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -699,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Rows' output: with a row tile per stream the thread's own; else the two
       // streams' halves of the keys joined, each warpgroup half of the columns.
-      float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + __log2f(l) : -CUDART_INF_F;
+      float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + (__log2f(l) - Held<E>::kUp) : -CUDART_INF_F;
       int c0 = 0, c1 = D;
       float inv = lse == -CUDART_INF_F ? 0.f : __fdividef(1.f, l);
       bool use0 = s == 0, use1 = s == 1;

@@ -565,7 +565,8 @@ int ft_qk_norm_rope(const ft_qk_args* args, void* stream);
  * keys, whose rows are not written.
  * Rows at or past q_start[num_reqs] are not written.  Scores, the softmax's
  * maximum and sum and the output's sum are held in 32 bits; the
- * probabilities are rounded to the cache's type for the second product.
+ * probabilities are rounded to the cache's type for the second product (f16
+ * probabilities below 2^-25 of a row's largest to multiples of 2^-35 of it).
  * q and out: [max_tokens, q_heads, head_dim] with rows q_stride / out_stride
  * elements apart (multiples of 16 bytes), in the cache's type.
  * workspace: ft_tree_attention_workspace bytes, 16-byte aligned, any contents;

@@ -850,3 +850,28 @@ def test_plan_columns_past_the_table_take_no_page(ft):
     assert r["table"].tolist() == [[7, 4], [8, 9], [5, 3]]
     assert r["slots"].tolist() == [7 * 16 + 10 + i for i in range(6)] + [4 * 16 + i for i in range(16)] + [-1] * 28 + \
         [-1] * 30 + [5 * 16 + 3 + i for i in range(13)] + [3 * 16] + [-1] * 6
+
+
+def test_attention_f16_long_tail_beside_one_large_score(ft):
+    """One key far above all others whose value is 0: the output is the others' 2^-25.5 each.  As many requests and
+    heads as a GPU has SMs, so that a CTA goes through thousands of keys beside the large one.
+
+    Probabilities are held in f16 as 2^11 of their share of the row's largest, so those below 2^-25 of it have a
+    fixed spacing of 2^-35: 2^-36 |v| a key, over the softmax sum."""
+    B, n_keys = 40, 16385
+    a = Attn(ft, [n_keys - 1] * B, [1] * B, 4, 4, 64, "f16", 64, mask="chain", seed=30, scale=1.0)
+    a.q.zero_()
+    a.q[:, :, 3] = 4.0
+    for page, row in a.rows:
+        k, v = torch.zeros((n_keys, 4, 64), device="cuda").half(), 1 + torch.rand((n_keys, 4, 64), device="cuda").half()
+        k[900, :, 3] = 25.5 * math.log(2) / 4
+        v[900] = 0
+        a.k[page, row], a.v[page, row] = k, v
+    a.run()
+    out, lse, mag, top = gpu_reference(a)
+    u = U["f16"]
+    tol = u * mag + u * np.abs(out) + 2.0 ** -16 * mag + 2.0 ** -36 * 2 * n_keys
+    got = a.out.double().cpu().numpy()
+    assert out.min() > 2e-4
+    assert (np.abs(got - out) <= tol).all(), np.max(np.abs(got - out) / tol)
+    assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()

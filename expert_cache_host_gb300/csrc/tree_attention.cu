@@ -94,7 +94,7 @@ struct Args {
   float c;                // |scale| log2 e
   bool neg;               // scale < 0
   float4* part_o;         // [2 grid][2 row tiles][D / 4][128 rows] of 4 outputs: a warp's rows are contiguous
-  float* part_lse;        // [2 grid][256], log2 units
+  float2* part_ml;        // [2 grid][256] a part's maximum m and sum l = sum 2^(c (S - m)), times 2^kUp
   struct Cut* cut;        // [grid] the item that begins at this CTA and goes on at the next
 };
 
@@ -104,7 +104,7 @@ struct Cut {
 };
 
 __host__ __device__ constexpr size_t cut_bytes(int grid) { return ((size_t)grid * sizeof(Cut) + 255) / 256 * 256; }
-__host__ __device__ constexpr size_t lse_bytes(int grid) { return (size_t)grid * 2 * 256 * 4; }
+__host__ __device__ constexpr size_t ml_bytes(int grid) { return (size_t)grid * 2 * 256 * sizeof(float2); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -239,7 +239,7 @@ struct Shared {
   uint32_t nonfinite[4];   // per item (mod 4): a new token's values held inf or NaN
   long long red[kThreads / 32];
   Walk start;              // where this CTA's share starts
-  float lse[2][128], inv[2][128];  // a row's streams: log2 sum with its maximum, 1 / sum
+  float m[2][128], l[2][128];  // a row's streams: maximum and sum
 };
 
 // The 32 bits of a token's visibility that begin at new token `off` (bits
@@ -713,33 +713,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Rows' output: with a row tile per stream the thread's own; else the two
       // streams' halves of the keys joined, each warpgroup half of the columns.
-      float w0 = s == 0 ? 1.f : 0.f, w1 = 1.f - w0, lse = l > 0.f || l != l ? m * g.c + (__log2f(l) - Held<E>::kUp) : -CUDART_INF_F;
+      // A sum is joined as its maximum and its sum: as one logarithm c m + log2 l
+      // it would lose l's bits to a large m (all of them at c m = 2^27).
+      float w0 = 0.f, w1 = 0.f;
       int c0 = 0, c1 = D;
-      float inv = lse == -CUDART_INF_F ? 0.f : __fdividef(1.f, l);
       bool use0 = s == 0, use1 = s == 1;
       if (!wk.pair) {
-        sh.lse[s][row] = cnt > 0 ? lse : -CUDART_INF_F;
-        sh.inv[s][row] = inv;
+        sh.m[s][row] = cnt > 0 ? m : -CUDART_INF_F;
+        sh.l[s][row] = l;
         bar_sync(1, 256);
-        const float l0 = sh.lse[0][row], l1 = sh.lse[1][row];
-        float top = fmaxf(l0, l1);
-        if (l0 != l0 || l1 != l1) top = CUDART_NAN_F;
-        if (top == -CUDART_INF_F) {
-          w0 = w1 = 0.f;
-          lse = top;
-        } else {
-          const float e0 = ex2(l0 - top), e1 = ex2(l1 - top);
-          lse = top + __log2f(e0 + e1);
-          const float f = __fdividef(1.f, e0 + e1);
-          w0 = e0 * f * sh.inv[0][row];
-          w1 = e1 * f * sh.inv[1][row];
-        }
-        use0 = l0 != -CUDART_INF_F;
-        use1 = l1 != -CUDART_INF_F;
+        const float m0 = sh.m[0][row], m1 = sh.m[1][row], l0 = sh.l[0][row], l1 = sh.l[1][row];
+        m = fmaxf(m0, m1);
+        use0 = m0 != -CUDART_INF_F;
+        use1 = m1 != -CUDART_INF_F;
+        w0 = use0 ? ex2((m0 - m) * g.c) : 0.f;
+        w1 = use1 ? ex2((m1 - m) * g.c) : 0.f;
+        l = (use0 ? w0 * l0 : 0.f) + (use1 ? w1 * l1 : 0.f);
         c0 = s * (D / 2);
         c1 = c0 + D / 2;
-        inv = 1.f;
       }
+      const bool some = l > 0.f || l != l;  // NaN: a seen score was NaN or +inf
+      const float inv = some ? __fdividef(1.f, l) : 0.f;
+      const float lse = some ? m * g.c + (__log2f(l) - Held<E>::kUp) : -CUDART_INF_F;
+      w0 *= inv;
+      w1 *= inv;
       // Written where an item has new keys, before the product of their tile: without row tile pairs the other
       // stream's warps know that it is only past the barrier above.
       const bool nonfinite = wk.t1 * KT > r.ctx && sh.nonfinite[item & 3];
@@ -804,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (valid && (wk.pair || s == 0)) {
         if (!whole)
-          g.part_lse[part_row] = lse;
+          g.part_ml[part_row] = make_float2(some ? m : -CUDART_INF_F, l);
         else if (a.lse)
           a.lse[(int64_t)(r.q0 + i) * a.q_heads + h0] = lse * kLn2;
       }
@@ -832,8 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that were cut; the blocks of a column share an
-// item.  With L_c a part's log2 sum and O_c its normalised output,
-// out = sum 2^(L_c - L) O_c, L = log2 sum 2^L_c.  The parts are in L2 and the
+// item.  With m_c, l_c a part's maximum and sum and O_c its normalised output,
+// M = max m_c, L = sum l_c 2^(c (m_c - M)), out = sum (l_c 2^(c (m_c - M)) / L) O_c
+// and ln sum = ln 2 (c M + log2 L).  The parts are in L2 and the
 // kernel is latency, so a batch's loads are all in flight before the first is
 // used, and where the item has few outputs several lanes share one (its parts in
 // stretches, joined in order).  A lane takes 4 outputs of a row.  Launched as a
@@ -841,12 +839,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 128, kJoinBlocks = 24, kJoinBatch = 8, kJoinSplit = 4;
 
 struct Part {
-  float top, sum;  // log2 reference, sum of 2^(L_c - top)
-  float4 acc;      // sum of 2^(L_c - top) O_c
-  __device__ __forceinline__ void move(float to) {
-    const float f = top == to ? 1.f : ex2(top - to);
-    top = to;
-    sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+  float m, l;  // maximum, sum
+  float4 acc;  // normalised output
+  __device__ __forceinline__ void scale(float w) { acc.x *= w, acc.y *= w, acc.z *= w, acc.w *= w; }
+  __device__ __forceinline__ void add(float w, const float4& o) {  // (o is not looked at where its weight is 0)
+    if (w > 0.f) acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y), acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
   }
 };
 
@@ -871,58 +868,63 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join_kernel(const
     Part q{-CUDART_INF_F, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     bool nan = false;
     for (int p0 = first; p0 < last; p0 += kJoinBatch) {
-      float l[kJoinBatch];
+      float2 ml[kJoinBatch];
       float4 o[kJoinBatch];
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
-        l[i] = -CUDART_INF_F;
+        ml[i] = make_float2(-CUDART_INF_F, 0.f);
         if (p0 + i < last) {
           const int at = slot(p0 + i);
-          l[i] = __ldcg(&g.part_lse[at * 256 + tile * 128 + row]);
+          ml[i] = __ldcg(&g.part_ml[at * 256 + tile * 128 + row]);
           o[i] = __ldcg(&g.part_o[((int64_t)(at * 2 + tile) * (D / 4) + col) * 128 + row]);
         }
       }
-      float most = q.top;
+      float most = q.m;
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
-        nan |= l[i] != l[i];
-        most = fmaxf(most, l[i]);
+        nan |= ml[i].y != ml[i].y;
+        most = fmaxf(most, ml[i].x);
       }
       if (most == -CUDART_INF_F) continue;
-      q.move(most);
+      const float was = q.l * ex2((q.m - most) * g.c);
+      float e[kJoinBatch], l = was;
 #pragma unroll
       for (int i = 0; i < kJoinBatch; ++i) {
-        const float e = ex2(l[i] - most);
-        if (e > 0.f) {
-          q.sum += e;
-          q.acc.x = fmaf(e, o[i].x, q.acc.x), q.acc.y = fmaf(e, o[i].y, q.acc.y);
-          q.acc.z = fmaf(e, o[i].z, q.acc.z), q.acc.w = fmaf(e, o[i].w, q.acc.w);
-        }
+        e[i] = ml[i].y * ex2((ml[i].x - most) * g.c);
+        l += e[i];
       }
+      const float inv = __fdividef(1.f, l);
+      q.scale(was * inv);
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) q.add(e[i] * inv, o[i]);
+      q.m = most, q.l = l;
     }
     // the stretches, lower parts first
     for (int s = per; s < 32; s *= 2) {
       Part r;
-      r.top = __shfl_down_sync(~0u, q.top, s);
-      r.sum = __shfl_down_sync(~0u, q.sum, s);
+      r.m = __shfl_down_sync(~0u, q.m, s);
+      r.l = __shfl_down_sync(~0u, q.l, s);
       r.acc.x = __shfl_down_sync(~0u, q.acc.x, s), r.acc.y = __shfl_down_sync(~0u, q.acc.y, s);
       r.acc.z = __shfl_down_sync(~0u, q.acc.z, s), r.acc.w = __shfl_down_sync(~0u, q.acc.w, s);
       nan |= __shfl_down_sync(~0u, (int)nan, s) != 0;
-      const float most = fmaxf(q.top, r.top);
+      const float most = fmaxf(q.m, r.m);
       if (most != -CUDART_INF_F) {
-        q.move(most), r.move(most);
-        q.sum += r.sum;
-        q.acc.x += r.acc.x, q.acc.y += r.acc.y, q.acc.z += r.acc.z, q.acc.w += r.acc.w;
+        const float a = q.l * ex2((q.m - most) * g.c), b = r.l * ex2((r.m - most) * g.c);
+        const float inv = __fdividef(1.f, a + b);
+        q.scale(a * inv);
+        q.add(b * inv, r.acc);
+        q.m = most, q.l = a + b;
       }
     }
     if (slice != 0 || x0 + lane >= outputs) continue;
-    if (nan) q.sum = CUDART_NAN_F;  // a part's scores held NaN: the row is NaN
-    const float inv = q.sum == 0.f ? 0.f : 1.f / q.sum;
+    if (nan) q.l = CUDART_NAN_F;  // a part's scores held NaN: the row is NaN
+    const float one = q.l != q.l ? q.l : 1.f;
     const int h = cut.h * g.G + row % g.G;
     const int64_t t = cut.token0 + tile * g.tpt + row / g.G;
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_stride + (int64_t)h * D + col * 4) =
-        make_uint2(Elem<E>::pack(q.acc.x * inv, q.acc.y * inv), Elem<E>::pack(q.acc.z * inv, q.acc.w * inv));
-    if (a.lse && col == 0) a.lse[t * a.q_heads + h] = q.sum == 0.f ? -CUDART_INF_F : (q.top + log2f(q.sum)) * kLn2;
+        make_uint2(Elem<E>::pack(q.acc.x * one, q.acc.y * one), Elem<E>::pack(q.acc.z * one, q.acc.w * one));
+    if (a.lse && col == 0)
+      a.lse[t * a.q_heads + h] = q.l == 0.f ? -CUDART_INF_F : (q.m * g.c + (log2f(q.l) - Held<E>::kUp)) * kLn2;
   }
 }
 
@@ -935,7 +937,7 @@ int check(const ft_attn_args& a) {
   return FT_OK;
 }
 
-uint64_t workspace(int grid, int D) { return cut_bytes(grid) + lse_bytes(grid) + (uint64_t)grid * 2 * 256 * D * 4; }
+uint64_t workspace(int grid, int D) { return cut_bytes(grid) + ml_bytes(grid) + (uint64_t)grid * 2 * 256 * D * 4; }
 
 bool cache_map(CUtensorMap* map, void* base, const ft_kv_cache& c, int64_t page, int64_t token, int64_t head, char* msg,
                size_t len) {
@@ -1028,8 +1030,8 @@ extern "C" int ft_tree_attention(const ft_attn_args* args, void* stream) {
   g.c = c > 1e-30f ? c : 1e-30f;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   g.cut = reinterpret_cast<Cut*>(ws);
-  g.part_lse = reinterpret_cast<float*>(ws + cut_bytes(grid));
-  g.part_o = reinterpret_cast<float4*>(ws + cut_bytes(grid) + lse_bytes(grid));
+  g.part_ml = reinterpret_cast<float2*>(ws + cut_bytes(grid));
+  g.part_o = reinterpret_cast<float4*>(ws + cut_bytes(grid) + ml_bytes(grid));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a.cache.dtype == FT_DTYPE_BF16)
     return D == 128 ? launch<__nv_bfloat16, 128>(g, grid, st) : launch<__nv_bfloat16, 64>(g, grid, st);

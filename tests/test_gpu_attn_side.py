@@ -875,3 +875,28 @@ def test_attention_f16_long_tail_beside_one_large_score(ft):
     assert out.min() > 2e-4
     assert (np.abs(got - out) <= tol).all(), np.max(np.abs(got - out) / tol)
     assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype", [
+    ([20000], [1], 8, 1, 128, "bf16"),            # parts of one and two key tiles, joined by the second kernel
+    ([9000, 3000], [3, 40], 8, 2, 64, "f16"),
+    ([300] * 200, [1] * 200, 8, 2, 128, "bf16"),  # two key tiles of one stream, one of the other
+])
+def test_attention_equal_scores_far_from_zero(ft, ctx, new, Hq, Hkv, D, dtype):
+    """All scores 2^26 (q.k 2^22 in f16, times 16): the output is the mean of what a row sees, however its keys are
+    split.  A sum held as one fp32 logarithm would round to a multiple of 8 there."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, 16, mask="chain", seed=31, scale=16.0)
+    a.q.zero_()
+    a.q[:, :, 1] = 1024.0
+    for rows in a.rows:
+        k = torch.zeros((len(rows[0]), Hkv, D), device="cuda", dtype=a.k.dtype)
+        k[:, :, 1] = 4096.0
+        a.k[rows] = k
+        tile = (torch.arange(len(rows[0]), device="cuda") // 128)[:, None, None]
+        a.v[rows] = a.v[rows].abs() * (1 + tile % 3)
+    a.run()
+    out, lse, mag, top = gpu_reference(a)
+    got, u = a.out.double().cpu().numpy(), U[dtype]
+    bad = np.abs(got - out) / (u * mag + u * np.abs(out) + 2.0 ** -16 * mag)
+    assert bad.max() <= 1, bad.max()
+    assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()

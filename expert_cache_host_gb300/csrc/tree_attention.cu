@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int cnt = wk.count(s);
       float m = -CUDART_INF_F, l = 0.f;
-      bool far = false;  // a row's m is past kFar
+      bool far = false;  // one of the warp's rows has m past kFar
       for (int j = 0; j < cnt; ++j, ++tiles_done) {
         if (!mbar_wait(&sh.s_full[s], tiles_done & 1, late)) late = true;
         tc_fence_after();
@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             l *= f;
             if (grow) m = top;
-            far = __any_sync(~0u, fabsf(m) * g.c > kFar && m != -CUDART_INF_F);
+            // (rows that are not this request's hold a neighbour's queries or none: no say in how these are rounded)
+            far = __any_sync(~0u, valid && fabsf(m) * g.c > kFar && m != -CUDART_INF_F);
           }
           float ref = m == -CUDART_INF_F ? 0.f : m * g.c;
           if (far) {

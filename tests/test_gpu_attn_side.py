@@ -900,3 +900,17 @@ def test_attention_equal_scores_far_from_zero(ft, ctx, new, Hq, Hkv, D, dtype):
     bad = np.abs(got - out) / (u * mag + u * np.abs(out) + 2.0 ** -16 * mag)
     assert bad.max() <= 1, bad.max()
     assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()
+
+
+def test_attention_of_a_request_does_not_depend_on_its_neighbours_numbers(ft):
+    """The next request's queries lie in the same tile of rows: whatever they are, this request's bits stay."""
+    n = 24
+    a = Attn(ft, [500, 30] * n, [1, 3] * n, 8, 1, 64, "bf16", 16, mask="chain", seed=32)
+    a.run()
+    out, lse = a.out.clone(), a.lse.clone()
+    mine = torch.arange(a.T, device="cuda") % 4 == 0
+    q = a.q.clone()
+    for value in (2.0e6, float("inf"), float("nan")):
+        a.q.copy_(torch.where(mine[:, None, None], q, q * value))
+        a.run()
+        assert torch.equal(a.out[mine], out[mine]) and torch.equal(a.lse[mine], lse[mine]), value

@@ -42,6 +42,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <limits>
 #include <type_traits>
 
 #include "attn_side.h"
@@ -1026,9 +1027,9 @@ extern "C" int ft_tree_attention(const ft_attn_args* args, void* stream) {
   g.G = a.q_heads / a.cache.kv_heads;
   g.tpt = 128 / g.G;
   g.neg = a.scale < 0.f;
-  // a scale of 0 keeps seen (0) and unseen (-inf) scores apart
+  // a scale of 0 becomes the least positive number: -inf stays -inf and the largest finite score is 5e-7
   const float c = (g.neg ? -a.scale : a.scale) * kLog2e;
-  g.c = c > 1e-30f ? c : 1e-30f;
+  g.c = c > 0.f ? c : std::numeric_limits<float>::denorm_min();
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   g.cut = reinterpret_cast<Cut*>(ws);
   g.part_ml = reinterpret_cast<float2*>(ws + cut_bytes(grid));

@@ -588,7 +588,7 @@ typedef struct ft_attn_args {
   int32_t q_heads;
   int32_t table_width;
   int32_t mask_words; /* new tokens of a request past 32*mask_words are seen by none; 0 without mask */
-  float scale;
+  float scale; /* any sign; |scale| < 1e37 */
   ft_kv_cache cache;
 } ft_attn_args;
 int ft_tree_attention(const ft_attn_args* args, void* stream);

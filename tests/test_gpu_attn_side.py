@@ -914,3 +914,12 @@ def test_attention_of_a_request_does_not_depend_on_its_neighbours_numbers(ft):
         a.q.copy_(torch.where(mine[:, None, None], q, q * value))
         a.run()
         assert torch.equal(a.out[mine], out[mine]) and torch.equal(a.lse[mine], lse[mine]), value
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-36])
+def test_attention_tiny_scales_of_large_products(ft, scale):
+    """Products of 1e33 times a scale of 0 or 1e-36 are scores near 0: every seen key counts alike."""
+    a = Attn(ft, [700, 33], [5, 20], 8, 2, 128, "bf16", 16, mask="tree", seed=33, scale=scale)
+    a.q.mul_(1e16)
+    a.k.mul_(1e16)
+    a.run().check()

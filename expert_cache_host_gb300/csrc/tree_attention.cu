@@ -29,8 +29,9 @@
 //    page (or per half of a head's 128 numbers), running ahead across items.
 //
 // Warps 0-3 and 4-7: softmax of stream 0 and 1 (a thread per row); warp 8: TMA;
-// warp 9: tensor-core issue; warp 10: V rows (below).  All waits are bounded
-// (FT_ST_TIMEOUT).
+// warp 9: tensor-core issue; warp 10: V rows (below).  All waits are bounded:
+// where one runs out (FT_ST_TIMEOUT) nothing more is loaded, and the CTA ends a
+// while after all its warps have come to theirs, with no copy or product in flight.
 //
 // Keys a row does not see get S = -inf by selection, so their bits do not
 // matter.  For V the product would turn 0 x NaN into NaN: rows of V past the
@@ -137,6 +138,8 @@ constexpr int kItemUnits = 6;
 struct Req {
   int q0, n, ctx, tiles, blocks;
 };
+// What copies and products in flight are given after a wait has run out; they take microseconds.
+constexpr uint64_t kDrainNs = 100000000;
 // Beyond this many keys a tile's end would not fit 31 bits.
 constexpr uint32_t kMostKeys = 0x7FFFFFFFu - 2 * KT;
 __device__ __forceinline__ Req request(const Args& g, int b) {
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++st == NST) st = 0, phase ^= 1;
           }
           page = next_page;
+          if (__any_sync(~0u, late)) wk.left = 0, wk.t1 = t;  // load nothing more
         }
       }
     } else if (warp == kFixer) {
@@ -824,10 +828,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && !has_cut) g.cut[blockIdx.x].parts = 0;
   }
   tc_fence_before();
-  __syncthreads();
+  const bool any_late = __syncthreads_or(late);
   tc_fence_after();
+  if (any_late) {
+    // Every copy and product that was issued has been waited for unless a wait
+    // ran out; those still in flight get kDrainNs.
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainNs;) __nanosleep(1000);
+    if (late && a.status) atomicOr(a.status, FT_ST_TIMEOUT);
+    __syncthreads();
+  }
   if (warp == kIssuer) tmem_dealloc(tmem, 512);
-  if (late && a.status) atomicOr(a.status, FT_ST_TIMEOUT);
 }
 
 // Joins the parts of the items that were cut; the blocks of a column share an

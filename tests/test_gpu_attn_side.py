@@ -923,3 +923,105 @@ def test_attention_tiny_scales_of_large_products(ft, scale):
     a.q.mul_(1e16)
     a.k.mul_(1e16)
     a.run().check()
+
+
+def far_apart(got, out, tol):
+    return np.abs(got - out) / tol
+
+
+LONG = [([33000, 128, 700], [17, 1, 5], 16, 2, 128, "bf16", 16, "token"),
+        ([30003], [3], 10, 2, 64, "f16", 64, "head"),
+        ([16000, 9000], [40, 1], 32, 4, 128, "f16", 128, "token"),
+        ([8000] * 6, [1, 33, 1, 64, 2, 1], 8, 1, 64, "bf16", 32, "head")]
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P,layout", LONG)
+def test_attention_every_value_tile_in_its_place(ft, ctx, new, Hq, Hkv, D, dtype, P, layout):
+    """A tile of 128 keys has values in a column of its own (tiles D apart share one), so that an output is the weight
+    of one or a few tiles and a tile left out or exchanged shows; the rows' values rise by half within a tile.
+
+    Tolerance: u = half spacing; every probability and the output are rounded once, u (sum p|v| + |o|), plus 2^-16
+    for scores and exponentials, plus in f16 2^-36 |v| a key over the softmax sum, and 2^-25 for an output below the
+    type's normal numbers."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, layout, mask="tree", seed=34)
+    values = []
+    for rows in a.rows:
+        key = torch.arange(len(rows[0]), device="cuda")
+        v = torch.zeros((len(key), Hkv, D), device="cuda", dtype=a.v.dtype)
+        v[key, :, (key // 128) % D] = (1 + (key % 128) / 256).to(a.v.dtype)[:, None]
+        a.v[rows] = v
+        values.append(v)
+    a.run()
+    out, lse, mag, top = gpu_reference(a)
+    got, u = a.out.double().cpu().numpy(), U[dtype]
+    tol = u * mag + u * np.abs(out) + 2.0 ** -16 * mag + 1e-30
+    if dtype == "f16":
+        keys = np.repeat([c + n for c, n in zip(ctx, new)], new)
+        total = np.exp(lse - top_scores(a))  # the softmax sum, its largest term 1
+        tol = tol + (2.0 ** -36 * 1.5 * keys[:, None] / total)[:, :, None] + 2.0 ** -25
+    bad = far_apart(got, out, tol)
+    assert bad.max() <= 1, (bad.max(), np.unravel_index(bad.argmax(), bad.shape))
+    assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()
+    # the same check refuses a reference with one tile of values lost, or those of another
+    b = int(np.argmax(ctx))
+    t0, rows = a.start[b], a.rows[b]
+    tiles = (ctx[b] + new[b]) // 128
+    for tile in (0, 1, tiles // 2, tiles - 1):
+        for other in (None, tile - 1 if tile else 1):
+            wrong = values[b].clone()
+            wrong[tile * 128:tile * 128 + 128] = 0 if other is None else values[b][other * 128:other * 128 + 128]
+            a.v[rows] = wrong
+            moved = gpu_reference(a)[0]
+            assert far_apart(got, moved, tol)[t0:t0 + new[b]].max(axis=(1, 2)).min() > 1, (tile, other)
+    a.v[rows] = values[b]
+
+
+def top_scores(a):
+    """The largest seen score of every row and head."""
+    out = np.zeros((a.T, a.Hq))
+    for b, (c, n) in enumerate(zip(a.ctx, a.new)):
+        k = a.k[a.rows[b]].double()
+        hidden = torch.zeros((n, c + n), dtype=torch.bool, device="cuda")
+        hidden[:, c:] = torch.from_numpy(~a.seen[b]).cuda()
+        t = slice(a.start[b], a.start[b] + n)
+        for h in range(a.Hq):
+            s = a.q[t, h].double() @ k[:, h * a.Hkv // a.Hq].T * a.scale
+            out[t, h] = s.masked_fill(hidden, -math.inf).amax(1).cpu().numpy()
+    return out
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P,layout", LONG)
+def test_attention_long_contexts_error_is_that_of_its_roundings(ft, ctx, new, Hq, Hkv, D, dtype, P, layout):
+    """Random values: the mean square error of a request's rows of one key head is that of independent roundings.
+
+    A rounding is at most u |x| and uniform, a mean square of u^2 x^2 / 3 or less: with e^2 = u^2 (sum p^2 v^2 + o^2) / 3
+    the mean of (err / e)^2 stays below 1; 1.15^2 leaves room for the spread of 1000 outputs and the fp32 steps.  A
+    tile of values lost or exchanged among 258 moves an output by 6 % of its size, 19 e and more."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, layout, mask="tree", seed=35).run()
+    out = gpu_reference(a)[0]
+    got, u, G = a.out.double().cpu().numpy(), U[dtype], Hq // Hkv
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        if c < 1000:
+            continue
+        k, v = (x[a.rows[b]].double() for x in (a.k, a.v))
+        hidden = torch.zeros((n, c + n), dtype=torch.bool, device="cuda")
+        hidden[:, c:] = torch.from_numpy(~a.seen[b]).cuda()
+        t = slice(a.start[b], a.start[b] + n)
+        for g in range(Hkv):
+            ratio = []
+            for h in range(g * G, g * G + G):
+                s = (a.q[t, h].double() @ k[:, g].T * a.scale).masked_fill(hidden, -math.inf)
+                pv = torch.softmax(s, 1) ** 2 @ v[:, g] ** 2
+                e2 = u * u * (pv.cpu().numpy() + out[t, h] ** 2) / 3
+                ratio.append((got[t, h] - out[t, h]) ** 2 / e2)
+            assert np.mean(ratio) <= 1.15 ** 2, (b, g, np.mean(ratio))
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P", [
+    ([0], [1500], 8, 2, 128, "bf16", 16), ([700], [1031], 4, 1, 64, "f16", 64), ([0, 129, 3], [513, 700, 2], 8, 8, 128, "f16", 128)])
+def test_attention_of_prompts(ft, ctx, new, Hq, Hkv, D, dtype, P):
+    """Without a mask: new tokens one after another, over several blocks of rows."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, mask="chain", seed=36).run()
+    a.reference = lambda: gpu_reference(a)
+    a.check()
+    assert a.status.item() == 0

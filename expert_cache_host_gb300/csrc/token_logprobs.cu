@@ -466,8 +466,9 @@ cudaError_t launch(const ft_logprob_args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_cs(const ft_logprob_args& a, cudaStream_t st) {
-  // A CTA for every SM, but none with less than one batch.  More CTAs shorten
-  // the read of a row and repeat the search for its alternatives: 61 rows of
+  // A CTA for every SM, but a row is halved again only where its stretches hold
+  // more than one batch each.  More CTAs shorten the read of a row and repeat the
+  // search for its alternatives: 61 rows of
   // 50021 fp32 take 6.9 us with 4 CTAs a row and 7.9 us with 8, 300 rows of
   // 131072 bf16 15.9 us with one and 23.4 us with 4.
   const int vecs = a.V / Logit<E>::N;

@@ -593,8 +593,10 @@ typedef struct ft_attn_args {
 } ft_attn_args;
 int ft_tree_attention(const ft_attn_args* args, void* stream);
 
-/* Workspace bytes for ft_tree_attention with these args' max_tokens, num_reqs,
- * q_heads and cache (pointers are not looked at). */
+/* Workspace bytes for ft_tree_attention with these args (pointers are not
+ * looked at).  The head size and the GPU's number of SMs decide, whatever the
+ * batch: two partial outputs of 256 rows an SM, about 40 MB at head_dim 128 on
+ * 152 SMs, so that one workspace serves every call of a stream. */
 int ft_tree_attention_workspace(const ft_attn_args* args, uint64_t* bytes);
 
 /* Scores of T rows of logits [T, V] (row_stride elements apart, any alignment

@@ -172,3 +172,15 @@ def test_struct_sizes_match_the_header():
         s = getattr(ft, n)
         want += [ctypes.sizeof(s)] + [getattr(s, f[0]).offset for f in s._fields_]
     assert got == want
+
+
+def test_workspace_follows_the_head_size_alone():
+    size = lambda **kw: ft.ft_tree_attention_workspace(attn(workspace=0, workspace_bytes=0, **kw))
+    n = size()
+    for kw in (dict(max_tokens=1), dict(max_tokens=100000), dict(num_reqs=1), dict(num_reqs=5000), dict(q_heads=2),
+               dict(q_heads=256), dict(mask=PTR, mask_words=4), dict(cache_kw=dict(dtype=ft.FT_DTYPE_F16)),
+               dict(cache_kw=dict(num_pages=100000)), dict(cache_kw=dict(page_size=64)), dict(cache_kw=dict(kv_heads=1))):
+        assert size(**kw) == n, kw
+    half = size(cache_kw=dict(head_dim=64))
+    # a part's maximum and sum (8 bytes a row) and the joins' list do not shrink with the head
+    assert n // 2 < half < n // 2 + n // 50

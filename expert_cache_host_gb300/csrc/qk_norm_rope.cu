@@ -11,7 +11,7 @@
 // that the token's angles and the weights are loaded once for ITER*HPW heads
 // and ITER 16-byte loads per lane are in flight before the first is used.
 // What is left is latency: 8192 tokens with 32/4 heads of 128 (172 MB) take
-// 32.2 us = 5.3 TB/s, a plain copy of the same bytes 25.9 us.
+// 32.0 us = 5.4 TB/s, a plain copy of the same bytes 25.9 us.
 //
 // With the whole head rotated in halves (i with i + D/2) a lane holds both
 // members of its pairs: elements 4l..4l+3 of either half.  The weights then go
@@ -29,8 +29,8 @@ namespace {
 
 constexpr int kWarps = 4;
 // Resident blocks per SM where there are many tokens (the most without spills).
-// 8192 tokens, 32/4 heads of 128: 32.2 us with 6, 33.9 with 5, 35.1 with 8.
-// 8000 tokens, 40/8 heads of 64, 32 rotated: 28.7 us with 5, 31.4 with 6.
+// 8192 tokens, 32/4 heads of 128: 32.0 us with 6, 33.8 with 5, 34.9 with 8.
+// 8000 tokens, 40/8 heads of 64, 32 rotated: 31.6 us with 5, 34.9 with 6.
 constexpr int kBlocks = 6, kBlocksOther = 5;
 
 struct Args {
@@ -290,7 +290,7 @@ cudaError_t launch(Args g, cudaStream_t st) {
   // Few tokens: one set per warp, so that a token spreads over the machine
   // (latency).  Many: four, so that angles and weights are loaded once for
   // four and four loads per lane are in flight, on resident warps that take
-  // one unit after another (512 tokens: 3.5 us, one set per warp 4.3; below,
+  // one unit after another (512 tokens: 3.4 us, one set per warp 4.1; below,
   // as fast).
   const bool many = (int64_t)g.a.T * sets >= (int64_t)sm_count() * 64;
   const int iter = many ? 4 : 1;

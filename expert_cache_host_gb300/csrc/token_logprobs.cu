@@ -469,8 +469,9 @@ cudaError_t launch_cs(const ft_logprob_args& a, cudaStream_t st) {
   // A CTA for every SM, but a row is halved again only where its stretches hold
   // more than one batch each.  More CTAs shorten the read of a row and repeat the
   // search for its alternatives: 61 rows of
-  // 50021 fp32 take 6.9 us with 4 CTAs a row and 7.9 us with 8, 300 rows of
-  // 131072 bf16 15.9 us with one and 23.4 us with 4.
+  // 50021 fp32 with 20 alternatives take 7.7 us with 4 CTAs a row, 9.1 with 8
+  // and 11.1 with one, 300 rows of 131072 bf16 with 8 alternatives 18.8 us with
+  // one and 27.1 us with 4.
   const int vecs = a.V / Logit<E>::N;
   int cs = 1;
   while (cs < kMaxCluster && (int64_t)a.T * cs < sm_count() && vecs / cs > kThreads * kVecs) cs *= 2;

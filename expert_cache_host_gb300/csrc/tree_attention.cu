@@ -9,12 +9,15 @@
 // product from there.
 //
 // What bounds it: K and V are read once from HBM and serve 128 or 256 rows.  A
-// 128-key tile is 64 KB at D = 128, 2750 cycles of one SM's share of HBM; its two
+// 128-key tile is 64 KB at D = 128, 1.49 us of one SM's share of HBM; its two
 // products take 1031 cycles per 128 rows.  So few rows leave it HBM-bound (32
-// single tokens over 16K keys, 1.07 GB: 168 us = 6.4 TB/s) and 256 rows bring
-// the products level with the reads (32 trees of 24..32 tokens over 8K..32K
-// keys, 1.37 GB, 0.30 TFLOP: 250 us = 5.5 TB/s, 1190 TFLOP/s; a tile takes 2700
-// cycles, 1320 of them one stream's softmax beside the other's products).  So:
+// single tokens over 16K keys, 1.07 GB: 168 us = 6.4 TB/s).  With 256 rows the
+// products take as long as the reads, and the chain from Q K^T over the softmax
+// (1320 cycles a row tile) to P V longer than either: 32 trees of 24..32 tokens
+// over 8K..32K keys, 1.37 GB, 0.30 TFLOP, take 254 us at best (5.4 TB/s) and
+// 275..285 us one call after another under the power cap (1612 MHz; 4.8 TB/s,
+// 1045 TFLOP/s), 2 us a tile where the reads need 1.49 us and the products
+// 1.28 us.  So:
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same
 //    amount of the flattened list of items, whatever the lengths (24 requests of
@@ -78,7 +81,7 @@ struct Held<__half> {
   static constexpr float kLag = 4.f, kUp = 11.f;
 };
 // The exponents c x - fl(c m) hold the rounding of c m, at most 2^-4 up to here;
-// past it (c m of 2^29 would overflow f16) they are c (x - m).
+// past it (at c m of 2^24 the rounding could overflow f16) they are c (x - m).
 constexpr float kFar = 1048576.f;
 
 template <int D>
@@ -127,12 +130,13 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 }
 
 // A tile costs a CTA this many units: with two row tiles the products and both
-// streams' softmax take 2700 cycles, with one 1750 (D = 128, measured).
+// streams' softmax take 2700 cycles, with one 1750 (measured at D = 128; used at
+// 64 too, where reads and products are half and the softmax is not).
 constexpr int kPairUnits = 3, kSingleUnits = 2;
 // An item costs this much besides (its Q, the first tile's way through the
 // pipeline, its output), counted after its tiles.  24 requests of 100..8192
-// keys: 39.2 us with 6, 40.3 with 3, 46.2 with 0; 40 requests of up to 3001 keys
-// and 37 tokens, f16, D = 64: 53.1, 61.6, 68.8.
+// keys: 40.2 us with 6, 41.5 with 3, 47.9 with 0; 40 requests of up to 3001 keys
+// and 37 tokens, f16, D = 64: 55.9, 64.4, 71.5.
 constexpr int kItemUnits = 6;
 // Requests' sizes and the walk over this CTA's work.
 struct Req {
@@ -693,6 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 t2 = split2(fma2(pair2(x[c], x[c + 1]), c2, ref2));
               const float p0 = ex2(t2.x), p1 = ex2(t2.y);
               sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pair2(p0, p1));
+              // 16 bits are what the second product takes; the sum keeps all 32.  Outputs are 2.3e-3 from 64 bits in
+              // bf16 and 2.8e-4 in f16, with 32-bit probabilities 1.7e-3 and 2.1e-4 (the output's own rounding).
               u[c >> 1] = Elem<E>::pack(p0, p1);
             }
             tmem_st32(t_s + half * 32, u + half * 32);

@@ -80,9 +80,11 @@ template <>
 struct Held<__half> {
   static constexpr float kLag = 4.f, kUp = 11.f;
 };
-// The exponents c x - fl(c m) hold the rounding of c m, at most 2^-4 up to here;
-// past it (at c m of 2^24 the rounding could overflow f16) they are c (x - m).
-constexpr float kFar = 1048576.f;
+// The exponents c x - fl(c m) hold the rounding of c m, and every maximum a row
+// has had, in either stream and in every part, has one of its own: up to here
+// two of them put a key's weight off by 2^-16 ln 2 at most.  Past it the
+// exponents are c (x - m).  (With 2^20 weights were off by up to 4 %.)
+constexpr float kFar = 256.f;
 
 template <int D>
 struct Cfg {

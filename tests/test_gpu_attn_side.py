@@ -1025,3 +1025,31 @@ def test_attention_of_prompts(ft, ctx, new, Hq, Hkv, D, dtype, P):
     a.reference = lambda: gpu_reference(a)
     a.check()
     assert a.status.item() == 0
+
+
+@pytest.mark.parametrize("base", [0, 2 ** 8, 2 ** 12, 2 ** 16, 2 ** 19, -2 ** 17])
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype", [
+    ([9000, 3000, 260], [3, 40, 1], 8, 2, 64, "f16"), ([20000], [1], 8, 1, 128, "f16"), ([700] * 160, [2] * 160, 8, 1, 128, "bf16")])
+def test_attention_small_differences_of_large_scores(ft, ctx, new, Hq, Hkv, D, dtype, base):
+    """Scores base + whole numbers of -16 .. 16, exact in fp32: what the base is changes nothing.
+
+    Keys are weighed against one another across rescalings, streams and parts; the tolerance is that of any scores."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, 16, mask="tree", seed=37, scale=1.0)
+    g = torch.Generator(device="cuda").manual_seed(38)
+    whole = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(a.q.dtype)
+    half = 2 ** (max(1, abs(base)).bit_length() // 2)
+    a.q.zero_()
+    a.q[:, :, 0], a.q[:, :, 1:5] = base / half, whole(a.T, Hq, 4)
+    for rows in a.rows:
+        k = torch.zeros((len(rows[0]), Hkv, D), device="cuda", dtype=a.k.dtype)
+        k[:, :, 0], k[:, :, 1:5] = half, whole(len(rows[0]), Hkv, 4)
+        a.k[rows] = k
+    a.run()
+    out, lse, mag, top = gpu_reference(a)
+    got, u = a.out.double().cpu().numpy(), U[dtype]
+    tol = u * mag + u * np.abs(out) + 2.0 ** -16 * mag
+    if dtype == "f16":  # values are below 6; the softmax sum is 1 and more
+        tol = tol + 2.0 ** -25 + 2.0 ** -36 * 6 * (max(ctx) + max(new))
+    bad = np.abs(got - out) / tol
+    assert bad.max() <= 1, (bad.max(), np.unravel_index(bad.argmax(), bad.shape))
+    assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()

@@ -83,7 +83,9 @@ struct Held<__half> {
 // The exponents c x - fl(c m) hold the rounding of c m, and every maximum a row
 // has had, in either stream and in every part, has one of its own: up to here
 // two of them put a key's weight off by 2^-16 ln 2 at most.  Past it the
-// exponents are c (x - m).  (With 2^20 weights were off by up to 4 %.)
+// exponents are c (x - m), 128 more subtractions a row and tile: 32 long trees
+// 287 us instead of 271, 24 requests 41.7 instead of 40.5.  (With 2^20 in place
+// of 256 weights were off by up to 4 %.)
 constexpr float kFar = 256.f;
 
 template <int D>

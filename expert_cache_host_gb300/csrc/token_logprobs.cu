@@ -429,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
     auto logp = [&](float x) {
       if (inf) return CUDART_NAN_F;
       if (empty || !(x > -CUDART_INF_F)) return -CUDART_INF_F;
-      return (x - s.m) - off;
+      return fminf((x - s.m) - off, 0.f);  // (a row of one entry: off is a rounding of either sign)
     };
     if (lane == 0) {
       if (a.status && (any_nan || inf)) atomicOr(a.status, FT_ST_NAN);
-      if (a.entropy) a.entropy[t] = inf ? CUDART_NAN_F : empty ? 0.f : kLn2 * (log2s - s.u / s.s);
+      if (a.entropy) a.entropy[t] = inf ? CUDART_NAN_F : empty ? 0.f : fmaxf(kLn2 * (log2s - s.u / s.s), 0.f);
       if (a.logprob && a.tokens) {
         if (token >= a.V && a.status) atomicOr(a.status, FT_ST_BAD_TOKEN);
         a.logprob[t] = token >= 0 && token < a.V ? logp(token_x) : CUDART_NAN_F;

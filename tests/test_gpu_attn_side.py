@@ -1053,3 +1053,22 @@ def test_attention_small_differences_of_large_scores(ft, ctx, new, Hq, Hkv, D, d
     bad = np.abs(got - out) / tol
     assert bad.max() <= 1, (bad.max(), np.unravel_index(bad.argmax(), bad.shape))
     assert (np.abs(a.lse.double().cpu().numpy() - lse) <= 2.0 ** -16 * top).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [9, 5003, 40000])
+def test_logprobs_stay_at_or_below_zero_and_entropies_at_or_above(ft, dtype, V):
+    """One logit far above all others, of every size: a probability is at most 1, whatever the sums' rounding."""
+    T = 500
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((T, V), generator=g, device="cuda")
+    tokens = torch.randint(0, V, (T,), generator=g, device="cuda").cpu().numpy()
+    size = torch.linspace(-900, 900, T, device="cuda") + torch.rand(T, generator=g, device="cuda")
+    x = x - 60 + size[:, None]
+    x[torch.arange(T), torch.from_numpy(tokens).cuda()] = size
+    x = x.to(DT[dtype])
+    got = run_logprob(ft, x, tokens, 3)
+    lp, ent, ids, lps = logprob_reference(x, tokens, 3)
+    for key, want in (("logprob", lp), ("entropy", ent), ("lps", lps)):
+        close(got[key], want)
+    assert got["logprob"].max() <= 0 and got["lps"].max() <= 0 and got["entropy"].min() >= 0

@@ -14,9 +14,9 @@
 // single tokens over 16K keys, 1.07 GB: 168 us = 6.4 TB/s).  With 256 rows the
 // products take as long as the reads, and the chain from Q K^T over the softmax
 // (1320 cycles a row tile) to P V longer than either: 32 trees of 24..32 tokens
-// over 8K..32K keys, 1.37 GB, 0.30 TFLOP, take 254 us at best (5.4 TB/s) and
-// 275..285 us one call after another under the power cap (1612 MHz; 4.8 TB/s,
-// 1045 TFLOP/s), 2 us a tile where the reads need 1.49 us and the products
+// over 8K..32K keys, 1.37 GB, 0.30 TFLOP, take 248..257 us at best and
+// 271..289 us one call after another under the power cap (285 us at 1612 MHz: 4.8
+// TB/s, 1045 TFLOP/s), 2 us a tile where the reads need 1.49 us and the products
 // 1.28 us.  So:
 //  - a work item (request, key head, block of up to 256 rows) is cut along the
 //    keys wherever the machine's even share ends: every CTA takes the same

@@ -107,6 +107,24 @@ class ft_logprob_args(ctypes.Structure):
                 _fields(ctypes.c_int64, "row_stride") + _fields(ctypes.c_int32, "dtype T V top_n"))
 
 
+class ft_kv8_cache(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "k v k_scale v_scale") +
+                _fields(ctypes.c_int32, "num_pages page_size block_size kv_heads head_dim reserved") +
+                _fields(ctypes.c_int64, "k_page_stride k_token_stride k_head_stride "
+                                        "v_page_stride v_token_stride v_head_stride"))
+
+
+class ft_kv8_store_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "k v q_start ctx_len block_table status") +
+                _fields(ctypes.c_int64, "k_stride v_stride") +
+                _fields(ctypes.c_int32, "dtype max_tokens num_reqs table_width") + [("cache", ft_kv8_cache)])
+
+
+class ft_kv8_load_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "k v slots status") + _fields(ctypes.c_int64, "k_stride v_stride") +
+                _fields(ctypes.c_int32, "dtype T") + [("cache", ft_kv8_cache)])
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -157,6 +175,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "ft_tree_attention": ([ctypes.POINTER(ft_attn_args), vp], i32),
             "ft_tree_attention_workspace": ([ctypes.POINTER(ft_attn_args), ctypes.POINTER(ctypes.c_uint64)], i32),
             "ft_token_logprobs": ([ctypes.POINTER(ft_logprob_args), vp], i32),
+            "ft_kv8_store": ([ctypes.POINTER(ft_kv8_store_args), vp], i32),
+            "ft_kv8_load": ([ctypes.POINTER(ft_kv8_load_args), vp], i32),
             "ft_last_error": ([], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -395,6 +415,18 @@ def make_logprob_args(**kw) -> ft_logprob_args:
     return _args(ft_logprob_args, kw)
 
 
+def make_kv8_cache(**kw) -> ft_kv8_cache:
+    return _args(ft_kv8_cache, kw)
+
+
+def make_kv8_store_args(**kw) -> ft_kv8_store_args:
+    return _args(ft_kv8_store_args, kw)
+
+
+def make_kv8_load_args(**kw) -> ft_kv8_load_args:
+    return _args(ft_kv8_load_args, kw)
+
+
 def ft_kv_plan(args: ft_plan_args, stream: int = 0) -> None:
     """Block tables, slots, positions and ancestor masks of a step."""
     _chk(load().ft_kv_plan(args, stream))
@@ -420,6 +452,16 @@ def ft_tree_attention(args: ft_attn_args, stream: int = 0) -> None:
 def ft_token_logprobs(args: ft_logprob_args, stream: int = 0) -> None:
     """Log probabilities of given tokens, entropy and top alternatives of rows of logits."""
     _chk(load().ft_token_logprobs(args, stream))
+
+
+def ft_kv8_store(args: ft_kv8_store_args, stream: int = 0) -> None:
+    """A step's keys and values quantised into the 8-bit paged cache."""
+    _chk(load().ft_kv8_store(args, stream))
+
+
+def ft_kv8_load(args: ft_kv8_load_args, stream: int = 0) -> None:
+    """Rows of the 8-bit paged cache read back in 16 bits."""
+    _chk(load().ft_kv8_load(args, stream))
 
 
 class HostPool:

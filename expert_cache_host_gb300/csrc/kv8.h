@@ -1,0 +1,62 @@
+// Shared by the operators on the 8-bit paged cache: e4m3 and scale-byte
+// conversions and the checks of a caller's ft_kv8_cache.
+#pragma once
+
+#include "attn_side.h"
+
+namespace ft {
+
+// 2^i for any i (0 below 2^-149).
+__device__ __forceinline__ float exp2i(int i) {
+  return i >= -126 ? __uint_as_float((uint32_t)(i + 127) << 23) : i >= -149 ? __uint_as_float(1u << (i + 149)) : 0.f;
+}
+// What a scale byte stands for.
+__device__ __forceinline__ float scale_of(uint32_t e) { return e == 255u ? __uint_as_float(0x7FC00000u) : exp2i((int)e - 127); }
+
+// Two e4m3 numbers (the low 16 bits) as f16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(v));
+  return r;
+}
+// Two floats rounded to e4m3 (nearest even; past 448 in size 448, NaN 0x7F), `lo` in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint32_t r;
+  asm("{ .reg .b16 h; cvt.rn.satfinite.e4m3x2.f32 h, %1, %2; cvt.u32.u16 %0, h; }" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+inline bool is_pow2(int x) { return x > 0 && !(x & (x - 1)); }
+inline int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+// FT_OK, or records why the cache cannot be used.
+inline int check_kv8_cache(const ft_kv8_cache& c) {
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return record_error(FT_E_ARG, "the cache's pointers must not be null");
+  if (c.reserved) return record_error(FT_E_ARG, "the cache's reserved field must be zero");
+  if (c.num_pages < 1 || c.kv_heads < 1 || c.head_dim < 1 || c.page_size < 1 || c.block_size < 1)
+    return record_error(FT_E_ARG, "num_pages, kv_heads, head_dim, page_size and block_size must be positive");
+  if (c.page_size < 16 || c.page_size > 4096 || !is_pow2(c.page_size))
+    return record_error(FT_E_UNSUPPORTED, "page_size must be a power of two, 16 to 4096 (got %d)", c.page_size);
+  if (c.block_size < 16 || c.block_size > 128 || !is_pow2(c.block_size) || c.block_size > c.page_size)
+    return record_error(FT_E_UNSUPPORTED, "block_size must be a power of two, 16 to 128 and at most page_size (got %d)",
+                        c.block_size);
+  if (c.head_dim != 64 && c.head_dim != 128)
+    return record_error(FT_E_UNSUPPORTED, "head_dim %d is not built", c.head_dim);
+  if (c.kv_heads > 16384) return record_error(FT_E_UNSUPPORTED, "more than 16384 key heads");
+  const int64_t s[6] = {c.k_page_stride, c.k_token_stride, c.k_head_stride,
+                        c.v_page_stride, c.v_token_stride, c.v_head_stride};
+  for (int64_t x : s)
+    if (x < 0 || x % 16 || x >= (int64_t(1) << 38))
+      return record_error(FT_E_ARG, "cache strides must be non-negative multiples of 16 bytes below 2^38");
+  if (!c.k_token_stride || !c.v_token_stride || (c.kv_heads > 1 && (!c.k_head_stride || !c.v_head_stride)) ||
+      (c.num_pages > 1 && (!c.k_page_stride || !c.v_page_stride)))
+    return record_error(FT_E_ARG, "the cache's rows, heads and pages must not share memory (a stride is 0)");
+  if (!is_16b(c.k) || !is_16b(c.v)) return record_error(FT_E_ARG, "the cache must be 16-byte aligned");
+  return FT_OK;
+}
+
+}  // namespace ft

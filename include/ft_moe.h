@@ -627,6 +627,91 @@ typedef struct ft_logprob_args {
 } ft_logprob_args;
 int ft_token_logprobs(const ft_logprob_args* args, void* stream);
 
+/* ---- A paged cache in 8 bits, and what accepts drafted tokens ----
+ *
+ * The same step over a cache of half the bytes: ft_kv8_store takes the keys and
+ * values that ft_qk_norm_rope would leave in a 16-bit cache (its cache argument
+ * can be a scratch of the step's rows, slots 0, 1, 2, ..), ft_kv8_attention
+ * reads them, ft_kv8_load gives rows back in 16 bits.  ft_verify_drafts takes
+ * the target's probabilities of the step's tokens and says which drafted tokens
+ * stay.  Conventions as above: no context, no state between calls, no
+ * synchronisation, capturable, lengths on the device. */
+
+/* One layer's paged key/value cache of e4m3 numbers (1 byte; sign, 4 exponent
+ * bits of bias 7, 3 fraction bits; 0x7F and 0xFF are NaN).  Rows lie as in
+ * ft_kv_cache, strides in bytes.  Rows [j*block_size, (j+1)*block_size) of a page
+ * and a head share one scale for keys and one for values: the byte
+ * k_scale[(page*(page_size/block_size) + j)*kv_heads + head] = e stands for
+ * 2^(e-127) (255: NaN), and a row's numbers are code * 2^(e-127). */
+typedef struct ft_kv8_cache {
+  void* k;
+  void* v;
+  uint8_t* k_scale; /* [num_pages, page_size/block_size, kv_heads] */
+  uint8_t* v_scale;
+  int32_t num_pages;  /* >= 1 */
+  int32_t page_size;  /* rows of a page: a power of two, 16 .. 4096 */
+  int32_t block_size; /* rows that share a scale: a power of two, 16 .. 128, at most page_size */
+  int32_t kv_heads;
+  int32_t head_dim; /* 64 or 128 */
+  int32_t reserved; /* must be zero */
+  int64_t k_page_stride, k_token_stride, k_head_stride; /* multiples of 16 */
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+} ft_kv8_cache;
+
+/* Quantises a step's keys and values as it writes them.  Request b's rows
+ * q_start[b] .. q_start[b+1]-1 become its tokens ctx_len[b], ctx_len[b]+1, ..,
+ * whose pages block_table[b] names (as ft_kv_plan leaves it).  For each head and
+ * each block of a request that gets rows, keys and values apart:
+ *   e = the least byte with max |x| <= 448 * 2^(e-127) over the block's new
+ *       finite numbers; where tokens below ctx_len[b] are in the block already,
+ *       the larger of that and the block's byte
+ *   code = x * 2^(127-e) rounded to e4m3 (nearest, ties to even); at most 240 in
+ *       size where 256 * 2^(e-127) would pass the range of the rows' type
+ * and where e grew the tokens already there are rounded again (exact but for
+ * numbers that become subnormal: at most half a step of 2^(e-127-9)).  Infinities
+ * and NaN become NaN and have no say in e.  A block whose byte is 255 is reported
+ * (FT_ST_NAN), its old tokens become NaN codes.  Rows of a block past the new
+ * ones stay.  A scale never shrinks while tokens below ctx_len share its block; a
+ * block that gets its first row starts anew.  Rows whose page is missing (outside
+ * the cache or past the table) are reported (FT_ST_BAD_SLOT) and left out.  Two
+ * requests of a call must not write into one block.
+ * k, v: [max_tokens, kv_heads, head_dim] of dtype, heads contiguous, rows
+ * k_stride / v_stride elements apart (multiples of 8, 16-byte aligned). */
+typedef struct ft_kv8_store_args {
+  const void* k;
+  const void* v;
+  const int32_t* q_start;     /* [num_reqs + 1] */
+  const int32_t* ctx_len;     /* [num_reqs] */
+  const int32_t* block_table; /* [num_reqs, table_width] */
+  uint32_t* status;
+  int64_t k_stride, v_stride;
+  int32_t dtype; /* FT_DTYPE_BF16 or FT_DTYPE_F16 */
+  int32_t max_tokens;
+  int32_t num_reqs;
+  int32_t table_width;
+  ft_kv8_cache cache;
+} ft_kv8_store_args;
+int ft_kv8_store(const ft_kv8_store_args* args, void* stream);
+
+/* Reads T rows of the cache back: k[t] and v[t] ([T, kv_heads, head_dim] of dtype)
+ * are the numbers at slots[t] (slot s: row s % page_size of page s / page_size),
+ * rounded to dtype (exact for what ft_kv8_store wrote from that type, but for
+ * numbers below its least normal one).  A negative slot gives zeros; so does one
+ * past the cache, which is reported (FT_ST_BAD_SLOT).  Slots may repeat.  Strides
+ * as for ft_kv8_store.  With ft_kv8_store it moves tokens: rows read back are
+ * stored again at their new places. */
+typedef struct ft_kv8_load_args {
+  void* k;
+  void* v;
+  const int64_t* slots; /* [T] */
+  uint32_t* status;
+  int64_t k_stride, v_stride;
+  int32_t dtype; /* FT_DTYPE_BF16 or FT_DTYPE_F16 */
+  int32_t T;
+  ft_kv8_cache cache;
+} ft_kv8_load_args;
+int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
+
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);
 

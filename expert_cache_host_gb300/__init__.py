@@ -125,6 +125,13 @@ class ft_kv8_load_args(ctypes.Structure):
                 _fields(ctypes.c_int32, "dtype T") + [("cache", ft_kv8_cache)])
 
 
+class ft_verify_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "probs draft_probs tokens parents accept_u draw_u q_start accepted n_accepted "
+                                         "next_token status") +
+                _fields(ctypes.c_int64, "probs_stride draft_stride") +
+                _fields(ctypes.c_int32, "dtype max_tokens num_reqs V"))
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -177,6 +184,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "ft_token_logprobs": ([ctypes.POINTER(ft_logprob_args), vp], i32),
             "ft_kv8_store": ([ctypes.POINTER(ft_kv8_store_args), vp], i32),
             "ft_kv8_load": ([ctypes.POINTER(ft_kv8_load_args), vp], i32),
+            "ft_verify_drafts": ([ctypes.POINTER(ft_verify_args), vp], i32),
             "ft_last_error": ([], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -427,6 +435,10 @@ def make_kv8_load_args(**kw) -> ft_kv8_load_args:
     return _args(ft_kv8_load_args, kw)
 
 
+def make_verify_args(**kw) -> ft_verify_args:
+    return _args(ft_verify_args, kw)
+
+
 def ft_kv_plan(args: ft_plan_args, stream: int = 0) -> None:
     """Block tables, slots, positions and ancestor masks of a step."""
     _chk(load().ft_kv_plan(args, stream))
@@ -462,6 +474,11 @@ def ft_kv8_store(args: ft_kv8_store_args, stream: int = 0) -> None:
 def ft_kv8_load(args: ft_kv8_load_args, stream: int = 0) -> None:
     """Rows of the 8-bit paged cache read back in 16 bits."""
     _chk(load().ft_kv8_load(args, stream))
+
+
+def ft_verify_drafts(args: ft_verify_args, stream: int = 0) -> None:
+    """Drafted tokens accepted or rejected by given random numbers, and the token that follows."""
+    _chk(load().ft_verify_drafts(args, stream))
 
 
 class HostPool:

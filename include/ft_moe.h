@@ -712,6 +712,54 @@ typedef struct ft_kv8_load_args {
 } ft_kv8_load_args;
 int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
 
+/* Which drafted tokens of a step stay, and the token that follows them, from the
+ * target's probabilities and given random numbers, so that what is said is
+ * distributed as the target's own.  Row 0 of a request is the last token told
+ * already, rows 1, 2, .. are drafted; parents as for ft_kv_plan (request-local
+ * indices below the row's own; NULL: each row's parent is the one before).
+ * probs[t] ([max_tokens, V], rows probs_stride elements apart) are the target's
+ * probabilities of what follows row t, as its sampler would draw from them (each
+ * entry in [0, 2], a row's sum about 1).  draft_probs[t] are those that the children
+ * of row t were drawn from, independently; NULL: the drafter had no choice (each
+ * child had probability 1).  From row 0 on, with a = probs, A = 1 at each row
+ * reached, its children x are tried in the order of their rows:
+ *   accepted, and the next row reached, if accept_u * q(x) * A < a(x)
+ *   otherwise a <- max(a - A q, 0), A <- sum a      (q = draft_probs of the row)
+ * Where no child is accepted the next token is drawn from a: the least i with
+ * a_0 + .. + a_i > draw_u * sum a (from probs where nothing of a is left).
+ *   accepted   [max_tokens] the request's accepted rows in order, from
+ *              accepted[q_start[b]] on, then -1
+ *   n_accepted [num_reqs], next_token [num_reqs]
+ * Rows whose parent is no row of theirs take no part.  Sums are exact to 2^-59 an
+ * entry (64-bit fixed point), so results do not depend on any order.  An entry
+ * outside [0, 2] counts as 0; it is reported (FT_ST_NAN) where it is met, and so is
+ * a row with nothing to draw from or a sum above 8: next_token is -1 there.  A
+ * drafted token outside [0, V) is reported (FT_ST_BAD_TOKEN) and takes no part; so
+ * does, reported as FT_ST_BAD_TREE, any child after the 64th that a row rejects.  A
+ * request without rows gets 0 and -1.  Rows at or past q_start[num_reqs] are not
+ * written.  accept_u [max_tokens] (row 0's is not used) and draw_u [num_reqs]: in
+ * [0, 1) (below 0 and NaN count as 0, from 1 on as the largest below 1).
+ * dtype: of probs and draft_probs. */
+typedef struct ft_verify_args {
+  const void* probs;
+  const void* draft_probs; /* or NULL */
+  const int32_t* tokens;   /* [max_tokens]; row 0's is not used */
+  const int32_t* parents;  /* [max_tokens] or NULL */
+  const float* accept_u;
+  const float* draw_u;
+  const int32_t* q_start; /* [num_reqs + 1] */
+  int32_t* accepted;
+  int32_t* n_accepted;
+  int32_t* next_token;
+  uint32_t* status;
+  int64_t probs_stride, draft_stride;
+  int32_t dtype; /* FT_DTYPE_F32, FT_DTYPE_BF16 or FT_DTYPE_F16 */
+  int32_t max_tokens;
+  int32_t num_reqs;
+  int32_t V;
+} ft_verify_args;
+int ft_verify_drafts(const ft_verify_args* args, void* stream);
+
 /* Message of the calling thread's last error ("" if none). */
 const char* ft_last_error(void);
 

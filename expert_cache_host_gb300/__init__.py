@@ -125,6 +125,13 @@ class ft_kv8_load_args(ctypes.Structure):
                 _fields(ctypes.c_int32, "dtype T") + [("cache", ft_kv8_cache)])
 
 
+class ft_kv8_attn_args(ctypes.Structure):
+    _fields_ = (_fields(ctypes.c_void_p, "q out lse q_start ctx_len block_table mask workspace status") +
+                _fields(ctypes.c_int64, "q_stride out_stride") + _fields(ctypes.c_uint64, "workspace_bytes") +
+                _fields(ctypes.c_int32, "dtype max_tokens max_new num_reqs q_heads table_width mask_words") +
+                [("scale", ctypes.c_float), ("cache", ft_kv8_cache)])
+
+
 class ft_verify_args(ctypes.Structure):
     _fields_ = (_fields(ctypes.c_void_p, "probs draft_probs tokens parents accept_u draw_u q_start accepted n_accepted "
                                          "next_token status") +
@@ -184,6 +191,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
             "ft_token_logprobs": ([ctypes.POINTER(ft_logprob_args), vp], i32),
             "ft_kv8_store": ([ctypes.POINTER(ft_kv8_store_args), vp], i32),
             "ft_kv8_load": ([ctypes.POINTER(ft_kv8_load_args), vp], i32),
+            "ft_kv8_attention": ([ctypes.POINTER(ft_kv8_attn_args), vp], i32),
+            "ft_kv8_attention_workspace": ([ctypes.POINTER(ft_kv8_attn_args), ctypes.POINTER(ctypes.c_uint64)], i32),
             "ft_verify_drafts": ([ctypes.POINTER(ft_verify_args), vp], i32),
             "ft_last_error": ([], ctypes.c_char_p),
         }
@@ -435,6 +444,10 @@ def make_kv8_load_args(**kw) -> ft_kv8_load_args:
     return _args(ft_kv8_load_args, kw)
 
 
+def make_kv8_attn_args(**kw) -> ft_kv8_attn_args:
+    return _args(ft_kv8_attn_args, kw)
+
+
 def make_verify_args(**kw) -> ft_verify_args:
     return _args(ft_verify_args, kw)
 
@@ -474,6 +487,18 @@ def ft_kv8_store(args: ft_kv8_store_args, stream: int = 0) -> None:
 def ft_kv8_load(args: ft_kv8_load_args, stream: int = 0) -> None:
     """Rows of the 8-bit paged cache read back in 16 bits."""
     _chk(load().ft_kv8_load(args, stream))
+
+
+def ft_kv8_attention_workspace(args: ft_kv8_attn_args) -> int:
+    """Bytes of the workspace ft_kv8_attention needs for these args' sizes."""
+    n = ctypes.c_uint64()
+    _chk(load().ft_kv8_attention_workspace(args, ctypes.byref(n)))
+    return n.value
+
+
+def ft_kv8_attention(args: ft_kv8_attn_args, stream: int = 0) -> None:
+    """Attention of a step's tokens (single, in sequence, or trees) over the 8-bit paged cache."""
+    _chk(load().ft_kv8_attention(args, stream))
 
 
 def ft_verify_drafts(args: ft_verify_args, stream: int = 0) -> None:

@@ -712,6 +712,45 @@ typedef struct ft_kv8_load_args {
 } ft_kv8_load_args;
 int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
 
+/* Attention of a step's tokens over an 8-bit paged cache (the new tokens' own keys
+ * and values already in it): as ft_tree_attention, with the cache's numbers
+ * code * 2^(e-127) in place of 16-bit ones and q and out of dtype.  Before the
+ * products the numbers are rounded to dtype, which keeps what ft_kv8_store wrote
+ * from it (of f16, numbers below 2^-14 have its fixed spacing of 2^-24); one past
+ * dtype's range counts as infinite, NaN codes and scale bytes of 255 as NaN.
+ * max_new: no request has more new tokens than this (0: max_tokens); one that has
+ * is reported (FT_ST_NO_ROOM) and its rows are not written.  A small max_new lets
+ * short rows take a kernel of their own.  workspace:
+ * ft_kv8_attention_workspace bytes, 16-byte aligned, any contents; calls that may
+ * overlap on the GPU need one each. */
+typedef struct ft_kv8_attn_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* q_start;     /* [num_reqs + 1] */
+  const int32_t* ctx_len;     /* [num_reqs] */
+  const int32_t* block_table; /* [num_reqs, table_width] */
+  const uint32_t* mask;       /* [max_tokens, mask_words] or NULL */
+  void* workspace;
+  uint32_t* status;
+  int64_t q_stride, out_stride;
+  uint64_t workspace_bytes;
+  int32_t dtype; /* FT_DTYPE_BF16 or FT_DTYPE_F16 */
+  int32_t max_tokens;
+  int32_t max_new;
+  int32_t num_reqs;
+  int32_t q_heads;
+  int32_t table_width;
+  int32_t mask_words; /* new tokens of a request past 32*mask_words are seen by none; 0 without mask */
+  float scale; /* any sign; |scale| < 1e37 */
+  ft_kv8_cache cache;
+} ft_kv8_attn_args;
+int ft_kv8_attention(const ft_kv8_attn_args* args, void* stream);
+
+/* Workspace bytes for ft_kv8_attention with these args (pointers are not looked
+ * at): the head size and the GPU's number of SMs decide. */
+int ft_kv8_attention_workspace(const ft_kv8_attn_args* args, uint64_t* bytes);
+
 /* Which drafted tokens of a step stay, and the token that follows them, from the
  * target's probabilities and given random numbers, so that what is said is
  * distributed as the target's own.  Row 0 of a request is the last token told

@@ -38,6 +38,14 @@ def load(cache_kw=None, **kw):
     return ft.make_kv8_load_args(**a)
 
 
+def attn(cache_kw=None, **kw):
+    a = dict(q=PTR, out=PTR, q_start=PTR, ctx_len=PTR, block_table=PTR, workspace=PTR, q_stride=1024, out_stride=1024,
+             workspace_bytes=1 << 40, dtype=ft.FT_DTYPE_BF16, max_tokens=3, max_new=0, num_reqs=2, q_heads=8, table_width=4,
+             mask_words=0, scale=0.1, cache=cache(**(cache_kw or {})))
+    a.update(kw)
+    return ft.make_kv8_attn_args(**a)
+
+
 def refused(call, args, code=ft.FT_E_ARG):
     with pytest.raises(ft.FtError) as ei:
         call(args)
@@ -62,6 +70,8 @@ BAD_CACHE = [(dict(k=0), ft.FT_E_ARG), (dict(v=0), ft.FT_E_ARG), (dict(k_scale=0
 def test_cache_refusals(kw, code):
     refused(ft.ft_kv8_store, store(cache_kw=kw), code)
     refused(ft.ft_kv8_load, load(cache_kw=kw), code)
+    refused(ft.ft_kv8_attention, attn(cache_kw=kw), code)
+    refused(ft.ft_kv8_attention_workspace, attn(cache_kw=kw), code)
 
 
 ROWS = [dict(k=0), dict(v=0), dict(k=PTR + 2), dict(v=PTR + 8), dict(k_stride=-8), dict(v_stride=257),
@@ -79,15 +89,42 @@ def test_load_refusals(kw):
     refused(ft.ft_kv8_load, load(**kw))
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(max_tokens=-1), ft.FT_E_ARG), (dict(max_new=-1), ft.FT_E_ARG), (dict(num_reqs=-1), ft.FT_E_ARG),
+    (dict(q_heads=0), ft.FT_E_ARG), (dict(q_heads=7), ft.FT_E_ARG), (dict(q_heads=2 * 129), ft.FT_E_UNSUPPORTED),
+    (dict(dtype=ft.FT_DTYPE_F32), ft.FT_E_ARG), (dict(q=0), ft.FT_E_ARG), (dict(out=0), ft.FT_E_ARG),
+    (dict(q_start=0), ft.FT_E_ARG), (dict(ctx_len=0), ft.FT_E_ARG), (dict(block_table=0), ft.FT_E_ARG),
+    (dict(workspace=0), ft.FT_E_ARG), (dict(workspace=PTR + 4), ft.FT_E_ARG), (dict(workspace_bytes=0), ft.FT_E_ARG),
+    (dict(q=PTR + 2), ft.FT_E_ARG), (dict(out=PTR + 2), ft.FT_E_ARG), (dict(q_stride=1023), ft.FT_E_ARG),
+    (dict(out_stride=1020), ft.FT_E_ARG), (dict(mask=PTR), ft.FT_E_ARG), (dict(mask_words=2), ft.FT_E_ARG),
+    (dict(table_width=0), ft.FT_E_ARG), (dict(scale=float("nan")), ft.FT_E_ARG), (dict(scale=float("inf")), ft.FT_E_ARG)],
+    ids=str)
+def test_attention_refusals(kw, code):
+    refused(ft.ft_kv8_attention, attn(**kw), code)
+
+
 def test_null_args_unknown_fields_and_no_rows():
     lib = ft.load()
-    for name in ("ft_kv8_store", "ft_kv8_load"):
+    for name in ("ft_kv8_store", "ft_kv8_load", "ft_kv8_attention"):
         assert getattr(lib, name)(None, None) == ft.FT_E_ARG
     with pytest.raises(TypeError):
         ft.make_kv8_store_args(no_such_field=1)
     ft.ft_kv8_store(store(max_tokens=0))
     ft.ft_kv8_store(store(num_reqs=0))
     ft.ft_kv8_load(load(T=0))
+    ft.ft_kv8_attention(attn(max_tokens=0))
+    ft.ft_kv8_attention(attn(num_reqs=0))
+    assert lib.ft_kv8_attention_workspace(None, None) == ft.FT_E_ARG
+
+
+def test_workspace_follows_the_head_size_alone():
+    size = lambda **kw: ft.ft_kv8_attention_workspace(attn(workspace=0, workspace_bytes=0, **kw))
+    n = size()
+    for kw in (dict(max_tokens=1), dict(max_tokens=100000), dict(max_new=1), dict(num_reqs=5000), dict(q_heads=256),
+               dict(mask=PTR, mask_words=4), dict(dtype=ft.FT_DTYPE_F16), dict(cache_kw=dict(num_pages=100000)),
+               dict(cache_kw=dict(page_size=64)), dict(cache_kw=dict(kv_heads=1))):
+        assert size(**kw) == n, kw
+    assert n % 16 == 0 and n // 2 <= size(cache_kw=dict(head_dim=64)) < n
 
 
 def struct_layout(names):
@@ -116,7 +153,7 @@ def struct_layout(names):
 
 
 def test_struct_sizes_match_the_header():
-    got, want = struct_layout(["ft_kv8_cache", "ft_kv8_store_args", "ft_kv8_load_args"])
+    got, want = struct_layout(["ft_kv8_cache", "ft_kv8_store_args", "ft_kv8_load_args", "ft_kv8_attn_args"])
     assert got == want
 
 

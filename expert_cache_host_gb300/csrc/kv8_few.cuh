@@ -1,0 +1,529 @@
+// Attention over the 8-bit paged cache where a request has few rows (new tokens
+// times the query heads of a key head: 16 at most), single tokens above all.
+//
+// Keys and values are read once for a handful of rows, so HBM bounds it and
+// everything else has to stay out of its way: 128 keys of a head are 32 KB at D =
+// 128, 0.75 us of one SM's share.  Tensor-core instructions with 128 rows would
+// need the codes as 16-bit numbers in shared memory (twice the bytes written and
+// read again); instead a warp takes 16 keys at a time from shared memory into
+// registers, where one instruction turns two codes into f16, as the operand with
+// 16 rows of m16n8k16, and the few query rows are the operand with 8:
+//   S^T = K Q^T [16 keys x 8 rows], O^T += V^T P^T [D x 8 rows]
+// The order of the head's numbers within a product is free, so a lane takes 16
+// contiguous codes of a key at a time and Q's fragments follow suit; P^T is
+// transposed within the warp.
+//
+// Scales stay out of the products: 16 keys lie in one block, so a chunk has one
+// scale for its keys, which the scores take, and one for its values, which the
+// probabilities take.  With X = s 2^ek, row maximum M and row offset mo:
+//   p = 2^(c (X - M)), l += p          and      P = 2^(c (X - M) + ev - mo + 11)
+// P in f16, where mo follows the maximum of c (X - M) + ev, so that a value's
+// weight is held relative to the largest weight times scale.  Queries are f16 too,
+// bf16 ones times a power of two of their row (the largest becomes 2^10: numbers
+// below 2^-34 of it are rounded to multiples of 2^-35).
+//
+// A CTA's eight warps take the eight chunks of a 128-key tile, each with a ring of
+// its own (cp.async) and no barrier before an item's end, where they are joined.
+#pragma once
+
+#include "tree_attention.cuh"
+
+namespace ft {
+namespace kv8_few {
+
+using tree_attention::Args;
+using tree_attention::Cut;
+using tree_attention::Deal;
+using tree_attention::Held;
+using tree_attention::kLn2;
+using tree_attention::KT;
+using tree_attention::Req;
+using tree_attention::uniform;
+using tree_attention::Walk;
+
+constexpr int kWarps = 8, kThreads = kWarps * 32, kChunk = 16;
+constexpr int kRows = 16;  // of a part
+constexpr float kUp = 11.f, kLagP = 4.f, kLagL = 8.f;  // P <= 2^15, p <= 2^8
+
+template <int D, int NB>
+struct Cfg {
+  static constexpr int R = 8 * NB;                        // rows
+  static constexpr int CTAS = NB == 1 ? 2 : 1;            // of an SM
+  static constexpr int HALF = kChunk * D;                 // bytes of a chunk's keys or values
+  static constexpr int STAGES = NB == 1 && D == 128 ? 3 : 4;
+  static constexpr int RING = kWarps * STAGES * 2 * HALF;
+  static constexpr int JOIN = kWarps * D * R * 4;         // the warps' outputs, in the ring's place
+  static constexpr int SMEM = RING > JOIN ? RING : JOIN;  // and Shared
+};
+
+template <int R>
+struct Shared {
+  long long red[kWarps];
+  Walk<true> start;
+  float m[kWarps][R], l[kWarps][R], mo[kWarps][R];
+  float f[kWarps][R];               // a warp's weight in the row
+  float most[R], sum[R], norm[R];   // the row's maximum and sum, and what its output is multiplied by, twice
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t lo2(uint32_t w) { return e4m3x2_to_f16x2(w & 0xFFFFu); }
+__device__ __forceinline__ uint32_t hi2(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
+// 2^i, infinite from 128 on.
+__device__ __forceinline__ float power(int i) { return i > 127 ? CUDART_INF_F : exp2i(i); }
+
+// Where a row's 16-byte piece lies in its chunk: such that the lanes that read
+// together (keys: rows g and g + 1, pieces t; values: rows 2t, pieces g) meet in
+// no bank.
+template <int D>
+__device__ __forceinline__ uint32_t place_k(int row, int piece) {
+  if constexpr (D == 128) return row * 128 + ((piece ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4);
+  return (row >> 1) * 128 + ((((row & 1) * 4 + piece) ^ (((row >> 1) & 3) * 2)) << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t place_v(int row, int piece) {
+  if constexpr (D == 128) return row * 128 + ((piece ^ (((row >> 1) & 3) * 2)) << 4);
+  return place_k<64>(row, piece);
+}
+
+template <typename E, int D, int NB>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(const __grid_constant__ Args g) {
+  using C = Cfg<D, NB>;
+  constexpr int R = C::R, S = C::STAGES, KS = D / 16, MT = D / 16;  // k steps of K Q^T, row tiles of V^T
+  constexpr bool BF = Elem<E>::kDtype == FT_DTYPE_BF16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Shared<R>& sh = *reinterpret_cast<Shared<R>*>(smem + C::SMEM);
+  const ft_attn_args& a = g.a;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  long long lo = 0;
+  Deal deal(0, 1);
+  tree_attention::schedule<true, kThreads>(g, sh.red, sh.start, lo, deal);
+  __syncthreads();
+  Walk<true> wk = sh.start;
+  const int share = wk.left;
+  bool has_cut = false;
+  uint8_t* const ring = smem + warp * S * 2 * C::HALF;
+  const uint32_t ring_at = smem_u32(ring);
+  const int page_mask = (1 << g.log2_page) - 1;
+
+  while (wk.next(g)) {
+    const Req& r = wk.r;
+    const int keys = r.ctx + r.n, rows = r.n * g.G, tiles = wk.t1 - wk.t0;
+    const int32_t* table = a.block_table + (int64_t)wk.b * a.table_width;
+    // The page of the warp's chunk of tile t; -1: none.
+    auto page_of = [&](int t) {
+      const int key0 = t * KT + warp * kChunk, col = key0 >> g.log2_page;
+      return t < wk.t1 && key0 < keys && col < a.table_width ? table[col] : -1;
+    };
+    int page = page_of(wk.t0);
+
+    // Queries, as the lane's numbers come in K's: pieces t4 and (D = 128) 4 + t4 of 16.
+    uint32_t qf[NB][KS][2];
+    int qe[NB];  // q = qf * 2^-qe
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = nb * 8 + gid, i = row / g.G;
+      uint4 w[D / 32];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) w[k] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (r.q0 + i) * a.q_stride + (int64_t)(wk.h * g.G + row - i * g.G) * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          w[k] = *reinterpret_cast<const uint4*>(q + (k >> 1) * 64 + t4 * 16 + (k & 1) * 8);
+      }
+      uint32_t u[D / 8];
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) u[4 * k] = w[k].x, u[4 * k + 1] = w[k].y, u[4 * k + 2] = w[k].z, u[4 * k + 3] = w[k].w;
+      qe[nb] = 0;
+      if constexpr (BF) {
+        uint32_t most = 0;  // the largest finite number's bits
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t x = u[k] & 0x7FFFu, y = u[k] >> 16 & 0x7FFFu;
+          most = max(most, max(x < 0x7F80u ? x : 0u, y < 0x7F80u ? y : 0u));
+        }
+        most = max(most, __shfl_xor_sync(~0u, most, 1));
+        most = max(most, __shfl_xor_sync(~0u, most, 2));
+        qe[nb] = most ? 137 - (int)max(most >> 7, 1u) : 0;  // the largest becomes 2^10 ..
+        const float f1 = exp2i(qe[nb] / 2), f2 = exp2i(qe[nb] - qe[nb] / 2);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float2 y = Elem<E>::unpack(u[k]);
+          u[k] = Elem<__half>::pack(y.x * f1 * f2, y.y * f1 * f2);
+        }
+      }
+      if (g.neg) {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) u[k] ^= 0x80008000u;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) qf[nb][k][0] = u[2 * k], qf[nb][k][1] = u[2 * k + 1];
+    }
+    // This thread's rows of the products, 2 t4 and 2 t4 + 1 of every eight: their queries' exponents, and which new
+    // tokens they see (16 at most).
+    int re[NB][2];
+    uint32_t vis[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        re[nb][j] = __shfl_sync(~0u, qe[nb], (2 * t4 + j) * 4);
+        const int row = nb * 8 + 2 * t4 + j, i = row / g.G;
+        vis[nb][j] = 0;
+        if (row < rows)
+          vis[nb][j] = (a.mask ? a.mask[(int64_t)(r.q0 + i) * a.mask_words] : (2u << i) - 1) & ((1u << r.n) - 1);
+      }
+    }
+
+    // The warp's chunk of tile t on its way into stage st; returns its scale bytes, or that there is none.
+    constexpr uint32_t kNone = 1u << 16;
+    auto issue = [&](int t, int st, int pg) -> uint32_t {
+      const int key0 = t * KT + warp * kChunk;
+      uint32_t bytes = kNone;
+      if (t < wk.t1 && key0 < keys) {
+        if (pg >= 0 && pg < a.cache.num_pages) {
+          const int row0 = key0 & page_mask;
+          const int64_t at = tree_attention::scale_index(g, pg, row0, wk.h);
+          const uint8_t* k = static_cast<const uint8_t*>(a.cache.k) + pg * a.cache.k_page_stride + wk.h * a.cache.k_head_stride;
+          const uint8_t* v = static_cast<const uint8_t*>(a.cache.v) + pg * a.cache.v_page_stride + wk.h * a.cache.v_head_stride;
+          const uint32_t to = ring_at + st * 2 * C::HALF;
+          constexpr int PIECES = D / 16, PER = 32 / PIECES;
+#pragma unroll
+          for (int i = 0; i < kChunk / PER; ++i) {
+            const int row = i * PER + lane / PIECES, piece = lane % PIECES;
+            const bool there = key0 + row < keys;  // rows past the end: zeros
+            copy16(to + place_k<D>(row, piece), k + (int64_t)(row0 + row) * a.cache.k_token_stride + piece * 16, there);
+            copy16(to + C::HALF + place_v<D>(row, piece), v + (int64_t)(row0 + row) * a.cache.v_token_stride + piece * 16, there);
+          }
+          bytes = __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
+        } else if (a.status && lane == 0) {
+          atomicOr(a.status, FT_ST_BAD_SLOT);
+        }
+      }
+      copy_commit();
+      return bytes;
+    };
+
+    uint32_t meta[S];  // the next chunks' scale bytes
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int after = page_of(wk.t0 + k + 1);
+      meta[k] = issue(wk.t0 + k, k, page);
+      page = after;
+    }
+
+    float M[NB][2], mo[NB][2], l[NB][2];
+    float o[MT][NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) M[nb][j] = mo[nb][j] = -CUDART_INF_F, l[nb][j] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < MT; ++k)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) o[k][nb][z] = 0.f;
+
+    int st = 0;
+#pragma unroll 1
+    for (int n = 0; n < tiles; ++n) {
+      const int t = wk.t0 + n, key0 = t * KT + warp * kChunk;
+      copy_wait<S - 1>();
+      __syncwarp();
+      const uint32_t bytes = meta[0];
+      if (!(bytes & kNone)) {
+        const uint8_t* kc = ring + st * 2 * C::HALF;
+        const uint8_t* vc = kc + C::HALF;
+        // scores of keys gid and gid + 8
+        float x[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) x[nb][z] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const uint4 p = *reinterpret_cast<const uint4*>(kc + place_k<D>(gid, k * 4 + t4));
+          const uint4 q = *reinterpret_cast<const uint4*>(kc + place_k<D>(gid + 8, k * 4 + t4));
+          const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = lo2(pw[w]), a1 = lo2(qw[w]), a2 = hi2(pw[w]), a3 = hi2(qw[w]);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) mma(x[nb], a0, a1, a2, a3, qf[nb][k * 4 + w][0], qf[nb][k * 4 + w][1]);
+          }
+        }
+        const int ek = (int)(bytes & 255u), ev = (int)(bytes >> 8 & 255u);
+        const float shift = ev == 255 ? CUDART_NAN_F : (float)(ev - 127);
+        const bool special = key0 + kChunk > r.ctx;  // new keys, or rows past the end
+        uint32_t seen[NB][2];                        // the row's keys of the chunk
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = ek == 255 ? CUDART_NAN_F : power(ek - 127 - re[nb][j]);
+            x[nb][j] *= f;
+            x[nb][2 + j] *= f;
+            seen[nb][j] = ~0u;
+            if (special) {
+              const int off = key0 - r.ctx;
+              seen[nb][j] = off < 0 ? vis[nb][j] << -off | ((1u << -off) - 1) : off < 32 ? vis[nb][j] >> off : 0u;
+              if (nb * 8 + 2 * t4 + j >= rows) seen[nb][j] = 0;
+              if (!(seen[nb][j] >> gid & 1)) x[nb][j] = -CUDART_INF_F;
+              if (!(seen[nb][j] >> (gid + 8) & 1)) x[nb][2 + j] = -CUDART_INF_F;
+            }
+          }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const float m = M[nb][z & 1], y = (x[nb][z] - m) * g.c;
+            grow |= x[nb][z] > -CUDART_INF_F && (m == -CUDART_INF_F || y > kLagL || y + shift - mo[nb][z & 1] > kLagP);
+          }
+        }
+        if (__any_sync(~0u, grow)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(x[nb][j], x[nb][2 + j]);
+              top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+              const float was = M[nb][j], m = fmaxf(was, top);
+              if (m > -CUDART_INF_F) {
+                const float down = was == -CUDART_INF_F ? 0.f : (was - m) * g.c;
+                const float before = mo[nb][j] + down, now = fmaxf(before, (top - m) * g.c + shift);
+                const float f = before == -CUDART_INF_F ? 1.f : ex2(before - now);
+                M[nb][j] = m;
+                mo[nb][j] = now;
+                l[nb][j] *= ex2(down);
+#pragma unroll
+                for (int k = 0; k < MT; ++k) o[k][nb][j] *= f, o[k][nb][2 + j] *= f;
+              }
+            }
+          }
+        }
+        uint32_t pf[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float w[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int j = z & 1;
+            const float m = M[nb][j] == -CUDART_INF_F ? 0.f : M[nb][j], off = mo[nb][j] == -CUDART_INF_F ? 0.f : mo[nb][j];
+            const float y = (x[nb][z] - m) * g.c;
+            l[nb][j] += ex2(y);
+            // 16 bits are what the product takes; the sum keeps all 32
+            w[z] = x[nb][z] == -CUDART_INF_F ? 0.f : ex2(y + (shift - off + kUp));
+          }
+          pf[nb][0] = transpose8(Elem<__half>::pack(w[0], w[1]));
+          pf[nb][1] = transpose8(Elem<__half>::pack(w[2], w[3]));
+        }
+        // values of keys 2 t4, 2 t4 + 1 and both + 8: the lane's D / 8 numbers from D / 8 gid on
+        uint32_t v[4][D / 32];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int row = 2 * t4 + (z & 1) + (z >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(vc + place_v<D>(row, gid));
+            v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(vc + place_v<D>(row, gid >> 1) + (gid & 1) * 8);
+            v[z][0] = u.x, v[z][1] = u.y;
+          }
+        }
+        if (special) {
+          // NaN codes of new tokens: out of the product (0 x NaN), and into the outputs of the rows that see them
+          uint32_t nan = 0;
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) nan |= ((v[z][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          if (__any_sync(~0u, nan != 0)) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+              for (int w = 0; w < D / 32; ++w)
+                v[z][w] &= ~((((v[z][w] & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xFFu);
+#pragma unroll 1
+            for (int key = 0; key < kChunk; ++key) {
+#pragma unroll
+              for (int b = 0; b < D / 8; ++b) {
+                const int d = gid * (D / 8) + b;
+                if ((vc[place_v<D>(key, d >> 4) + (d & 15)] & 0x7F) != 0x7F) continue;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+                    if (seen[nb][j] >> key & 1) o[b >> 1][nb][(b & 1) * 2 + j] = CUDART_NAN_F;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t p0 = __byte_perm(v[0][w], v[1][w], 0x5140), p1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t q0 = __byte_perm(v[2][w], v[3][w], 0x5140), q1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          const uint32_t f0[4] = {lo2(p0), hi2(p0), lo2(q0), hi2(q0)}, f1[4] = {lo2(p1), hi2(p1), lo2(q1), hi2(q1)};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma(o[2 * w][nb], f0[0], f0[1], f0[2], f0[3], pf[nb][0], pf[nb][1]);
+            mma(o[2 * w + 1][nb], f1[0], f1[1], f1[2], f1[3], pf[nb][0], pf[nb][1]);
+          }
+        }
+      }
+      __syncwarp();
+      const int after = page_of(t + S + 1);
+      const uint32_t next = issue(t + S, st, page);
+      page = after;
+#pragma unroll
+      for (int k = 0; k + 1 < S; ++k) meta[k] = meta[k + 1];
+      meta[S - 1] = next;
+      if (++st == S) st = 0;
+    }
+    copy_wait<0>();
+
+    // The warps' sums joined: in the rings' place, [warp][number of a lane][gid][row].
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float s = l[nb][j];
+        s += __shfl_xor_sync(~0u, s, 4);
+        s += __shfl_xor_sync(~0u, s, 8);
+        s += __shfl_xor_sync(~0u, s, 16);
+        const int row = nb * 8 + 2 * t4 + j;
+        if (gid == 0) sh.m[warp][row] = M[nb][j], sh.l[warp][row] = s, sh.mo[warp][row] = mo[nb][j];
+      }
+    }
+    __syncthreads();  // the rings are empty
+    float* const outs = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float* to = outs + ((warp * (D / 8) + 2 * k) * 8 + gid) * R + nb * 8 + 2 * t4;
+        *reinterpret_cast<float2*>(to) = make_float2(o[k][nb][0], o[k][nb][1]);
+        *reinterpret_cast<float2*>(to + 8 * R) = make_float2(o[k][nb][2], o[k][nb][3]);
+      }
+    }
+    if (tid < R) {
+      float m = -CUDART_INF_F, sum = 0.f, off = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.m[w][tid]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sh.m[w][tid];
+        const bool some = mw != -CUDART_INF_F || sh.l[w][tid] != 0.f;
+        const float down = mw == -CUDART_INF_F ? 0.f : (mw - m) * g.c;
+        if (some) sum += sh.l[w][tid] * ex2(down);
+        off = fmaxf(off, sh.mo[w][tid] + down);
+      }
+      if (off == -CUDART_INF_F) off = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sh.m[w][tid], down = mw == -CUDART_INF_F ? 0.f : (mw - m) * g.c;
+        const bool some = mw != -CUDART_INF_F || sh.l[w][tid] != 0.f;
+        const float at = sh.mo[w][tid] == -CUDART_INF_F ? 0.f : sh.mo[w][tid] + down - off;
+        sh.f[w][tid] = some ? ex2(at) : 0.f;
+      }
+      sh.most[tid] = m;
+      sh.sum[tid] = sum;
+      sh.norm[tid] = ex2(0.5f * (off - kUp));  // (its square may be below what fp32 holds)
+    }
+    __syncthreads();
+    const bool whole = wk.t0 == 0 && wk.t1 == r.tiles;
+    const int slot = blockIdx.x * 2 + (wk.t0 == 0 ? 1 : 0);
+    for (int z = tid; z < rows * (D / 4); z += kThreads) {
+      const int col = z / rows, row = z - col * rows;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = sh.f[w][row];
+        if (f == 0.f) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int d = col * 4 + k;
+          y[k] += f * outs[((w * (D / 8) + d % (D / 8)) * 8 + d / (D / 8)) * R + row];
+        }
+      }
+      const float sum = sh.sum[row], norm = sh.norm[row];
+      const bool some = sum > 0.f || sum != sum;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = some ? y[k] * norm / sum * norm : 0.f;
+      const int i = row / g.G, head = wk.h * g.G + row - i * g.G;
+      if (whole) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (r.q0 + i) * a.out_stride + (int64_t)head * D + col * 4) =
+            make_uint2(Elem<E>::pack(y[0], y[1]), Elem<E>::pack(y[2], y[3]));
+        if (a.lse && col == 0)
+          a.lse[(int64_t)(r.q0 + i) * a.q_heads + head] = some ? (sh.most[row] * g.c + log2f(sum)) * kLn2 : -CUDART_INF_F;
+      } else {
+        g.part_o[((int64_t)slot * (D / 4) + col) * kRows + row] = make_float4(y[0], y[1], y[2], y[3]);
+        if (col == 0)
+          g.part_ml[slot * kRows + row] =
+              make_float2(some ? sh.most[row] : -CUDART_INF_F, sum * (Held<E>::kUp == 0.f ? 1.f : 2048.f));
+      }
+    }
+    if (!whole && wk.t0 == 0) {
+      has_cut = true;
+      if (tid == 0) {
+        // the CTA that owns the first unit of the item's last tile
+        const long long it = lo + (share - wk.left) - wk.unit + (long long)(r.tiles - 1) * wk.weight();
+        g.cut[blockIdx.x] = Cut{deal.owner(it) - (int)blockIdx.x + 1, rows, r.q0, wk.h};
+      }
+    }
+    __syncthreads();  // the outputs have been read
+  }
+  if (tid == 0 && !has_cut) g.cut[blockIdx.x].parts = 0;
+}
+
+template <typename E, int D, int NB>
+int launch(const Args& g, int grid, cudaStream_t st) {
+  using C = Cfg<D, NB>;
+  constexpr int smem = C::SMEM + (int)sizeof(Shared<C::R>);
+  static_assert(smem * C::CTAS <= 227 * 1024, "the CTAs of an SM must fit its shared memory");
+  static_assert(Held<__half>::kUp == 11.f && Held<__nv_bfloat16>::kUp == 0.f, "parts' sums are scaled by 2^kUp");
+  static thread_local int configured = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e = cudaFuncSetAttribute(few_rows_kernel<E, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention setup failed: %s", cudaGetErrorString(e));
+    configured = dev;
+  }
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  pdl_config(cfg, attr, dim3(grid), dim3(kThreads), smem, st);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<E, D, NB>, g);
+  if (e == cudaSuccess) e = tree_attention::launch_join<E, D, kRows>(g, grid, st);
+  if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+  return FT_OK;
+}
+
+}  // namespace kv8_few
+}  // namespace ft

@@ -714,10 +714,11 @@ int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
 
 /* Attention of a step's tokens over an 8-bit paged cache (the new tokens' own keys
  * and values already in it): as ft_tree_attention, with the cache's numbers
- * code * 2^(e-127) in place of 16-bit ones and q and out of dtype.  Before the
- * products the numbers are rounded to dtype, which keeps what ft_kv8_store wrote
+ * code * 2^(e-127) in place of 16-bit ones and q and out of dtype.  The numbers may
+ * be rounded to dtype before the products, which keeps what ft_kv8_store wrote
  * from it (of f16, numbers below 2^-14 have its fixed spacing of 2^-24); one past
- * dtype's range counts as infinite, NaN codes and scale bytes of 255 as NaN.
+ * dtype's range may then count as infinite.  NaN codes and scale bytes of 255 are
+ * NaN.
  * max_new: no request has more new tokens than this (0: max_tokens); one that has
  * is reported (FT_ST_NO_ROOM) and its rows are not written.  A small max_new lets
  * short rows take a kernel of their own.  workspace:

@@ -23,7 +23,8 @@
 // below 2^-34 of it are rounded to multiples of 2^-35).
 //
 // A CTA's eight warps take the eight chunks of a 128-key tile, each with a ring of
-// its own (cp.async) and no barrier before an item's end, where they are joined.
+// its own (TMA) and no barrier of the CTA before an item's end, where they are
+// joined.  All waits are bounded, as in tree_attention.cuh.
 #pragma once
 
 #include "tree_attention.cuh"
@@ -56,23 +57,15 @@ struct Cfg {
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;  // and Shared
 };
 
-template <int R>
+template <int R, int S>
 struct Shared {
+  uint64_t full[kWarps][S];
   long long red[kWarps];
   Walk<true> start;
   float m[kWarps][R], l[kWarps][R], mo[kWarps][R];
   float f[kWarps][R];               // a warp's weight in the row
   float most[R], sum[R], norm[R];   // the row's maximum and sum, and what its output is multiplied by, twice
 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -85,34 +78,36 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t lo2(uint32_t w) { return e4m3x2_to_f16x2(w & 0xFFFFu); }
-__device__ __forceinline__ uint32_t hi2(uint32_t w) { return e4m3x2_to_f16x2(w >> 16); }
-// 2^i, infinite from 128 on.
-__device__ __forceinline__ float power(int i) { return i > 127 ? CUDART_INF_F : exp2i(i); }
-
-// Where a row's 16-byte piece lies in its chunk: such that the lanes that read
-// together (keys: rows g and g + 1, pieces t; values: rows 2t, pieces g) meet in
-// no bank.
-template <int D>
-__device__ __forceinline__ uint32_t place_k(int row, int piece) {
-  if constexpr (D == 128) return row * 128 + ((piece ^ (((row & 1) << 2) | ((row >> 1) & 3))) << 4);
-  return (row >> 1) * 128 + ((((row & 1) * 4 + piece) ^ (((row >> 1) & 3) * 2)) << 4);
+// Four codes as f16: the lower two, the upper two.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
+
+// Where a row's 16-byte piece lies in its chunk (the swizzle of D bytes).  The
+// lanes that read together (keys: two rows, every second or every piece; values:
+// every second row, two pieces) meet in no bank at D = 128, values' in twos at 64.
 template <int D>
-__device__ __forceinline__ uint32_t place_v(int row, int piece) {
-  if constexpr (D == 128) return row * 128 + ((piece ^ (((row >> 1) & 3) * 2)) << 4);
-  return place_k<64>(row, piece);
+__device__ __forceinline__ uint32_t place(int row, int piece) {
+  if constexpr (D == 128) return row * 128 + ((piece ^ (row & 7)) << 4);
+  return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
 template <typename E, int D, int NB>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(const __grid_constant__ Args g) {
+__global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(const __grid_constant__ CUtensorMap map_k,
+                                                                                     const __grid_constant__ CUtensorMap map_v,
+                                                                                     const __grid_constant__ Args g) {
   using C = Cfg<D, NB>;
   constexpr int R = C::R, S = C::STAGES, KS = D / 16, MT = D / 16;  // k steps of K Q^T, row tiles of V^T
   constexpr bool BF = Elem<E>::kDtype == FT_DTYPE_BF16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  Shared<R>& sh = *reinterpret_cast<Shared<R>*>(smem + C::SMEM);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Shared<R, S>& sh = *reinterpret_cast<Shared<R, S>*>(smem + C::SMEM);
   const ft_attn_args& a = g.a;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+  if (lane < S) mbar_init(&sh.full[warp][lane], 1);
+  mbar_init_fence();
+  if (tid < 2) tree_attention::prefetch_map(tid ? &map_v : &map_k);
   pdl_wait();
   pdl_trigger();
   long long lo = 0;
@@ -121,10 +116,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
   __syncthreads();
   Walk<true> wk = sh.start;
   const int share = wk.left;
-  bool has_cut = false;
+  bool has_cut = false, late = false;
+  uint32_t parity = 0;  // a bit per stage: of its next filling
   uint8_t* const ring = smem + warp * S * 2 * C::HALF;
-  const uint32_t ring_at = smem_u32(ring);
   const int page_mask = (1 << g.log2_page) - 1;
+  // This lane's pieces of a chunk: of keys gid (and 8 rows on, gid + 8), of values in rows 2 t4 (and 1, 8, 9 on).
+  uint32_t k_at[D / 64], v_at[2];
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) k_at[k] = place<D>(gid, D == 128 ? 2 * t4 + k : t4);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    v_at[k] = C::HALF + (D == 128 ? place<D>(2 * t4 + k, gid) : place<D>(2 * t4 + k, gid >> 1) + (gid & 1) * 8);
+  constexpr uint32_t kOn = 8 * D;  // 8 rows on, in the same places of the swizzle
 
   while (wk.next(g)) {
     const Req& r = wk.r;
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     };
     int page = page_of(wk.t0);
 
-    // Queries, as the lane's numbers come in K's: pieces t4 and (D = 128) 4 + t4 of 16.
+    // Queries, as the lane's numbers come in K's: D / 4 from D / 4 t4 on.
     uint32_t qf[NB][KS][2];
     int qe[NB];  // q = qf * 2^-qe
 #pragma unroll
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + (r.q0 + i) * a.q_stride + (int64_t)(wk.h * g.G + row - i * g.G) * D;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
-          w[k] = *reinterpret_cast<const uint4*>(q + (k >> 1) * 64 + t4 * 16 + (k & 1) * 8);
+          w[k] = *reinterpret_cast<const uint4*>(q + t4 * (D / 4) + k * 8);
       }
       uint32_t u[D / 8];
 #pragma unroll
@@ -182,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     }
     // This thread's rows of the products, 2 t4 and 2 t4 + 1 of every eight: their queries' exponents, and which new
     // tokens they see (16 at most).
-    int re[NB][2];
+    float rf[NB][2];
     uint32_t vis[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        re[nb][j] = __shfl_sync(~0u, qe[nb], (2 * t4 + j) * 4);
+        rf[nb][j] = exp2i(-__shfl_sync(~0u, qe[nb], (2 * t4 + j) * 4));
         const int row = nb * 8 + 2 * t4 + j, i = row / g.G;
         vis[nb][j] = 0;
         if (row < rows)
@@ -200,29 +203,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     constexpr uint32_t kNone = 1u << 16;
     auto issue = [&](int t, int st, int pg) -> uint32_t {
       const int key0 = t * KT + warp * kChunk;
-      uint32_t bytes = kNone;
-      if (t < wk.t1 && key0 < keys) {
-        if (pg >= 0 && pg < a.cache.num_pages) {
-          const int row0 = key0 & page_mask;
-          const int64_t at = tree_attention::scale_index(g, pg, row0, wk.h);
-          const uint8_t* k = static_cast<const uint8_t*>(a.cache.k) + pg * a.cache.k_page_stride + wk.h * a.cache.k_head_stride;
-          const uint8_t* v = static_cast<const uint8_t*>(a.cache.v) + pg * a.cache.v_page_stride + wk.h * a.cache.v_head_stride;
-          const uint32_t to = ring_at + st * 2 * C::HALF;
-          constexpr int PIECES = D / 16, PER = 32 / PIECES;
-#pragma unroll
-          for (int i = 0; i < kChunk / PER; ++i) {
-            const int row = i * PER + lane / PIECES, piece = lane % PIECES;
-            const bool there = key0 + row < keys;  // rows past the end: zeros
-            copy16(to + place_k<D>(row, piece), k + (int64_t)(row0 + row) * a.cache.k_token_stride + piece * 16, there);
-            copy16(to + C::HALF + place_v<D>(row, piece), v + (int64_t)(row0 + row) * a.cache.v_token_stride + piece * 16, there);
-          }
-          bytes = __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
-        } else if (a.status && lane == 0) {
-          atomicOr(a.status, FT_ST_BAD_SLOT);
-        }
+      if (t >= wk.t1 || key0 >= keys || late) return kNone;
+      if (pg < 0 || pg >= a.cache.num_pages) {
+        if (a.status && lane == 0) atomicOr(a.status, FT_ST_BAD_SLOT);
+        return kNone;
       }
-      copy_commit();
-      return bytes;
+      const int row0 = key0 & page_mask;
+      if (lane == 0) {
+        mbar_expect_tx(&sh.full[warp][st], 2 * C::HALF);
+        tensor_g2s_4d(ring + st * 2 * C::HALF, &map_k, 0, row0, wk.h, pg, &sh.full[warp][st]);
+        tensor_g2s_4d(ring + st * 2 * C::HALF + C::HALF, &map_v, 0, row0, wk.h, pg, &sh.full[warp][st]);
+      }
+      const int64_t at = tree_attention::scale_index(g, pg, row0, wk.h);
+      return __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
     };
 
     uint32_t meta[S];  // the next chunks' scale bytes
@@ -233,12 +226,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
       page = after;
     }
 
-    float M[NB][2], mo[NB][2], l[NB][2];
+    // A row's maximum and offset as they are and (0 where there is none yet) as they are used.
+    float M[NB][2], mo[NB][2], l[NB][2], Mr[NB][2], up[NB][2];
     float o[MT][NB][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) M[nb][j] = mo[nb][j] = -CUDART_INF_F, l[nb][j] = 0.f;
+      for (int j = 0; j < 2; ++j) M[nb][j] = mo[nb][j] = -CUDART_INF_F, l[nb][j] = Mr[nb][j] = 0.f, up[nb][j] = kUp;
     }
 #pragma unroll
     for (int k = 0; k < MT; ++k)
@@ -251,12 +245,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
 #pragma unroll 1
     for (int n = 0; n < tiles; ++n) {
       const int t = wk.t0 + n, key0 = t * KT + warp * kChunk;
-      copy_wait<S - 1>();
-      __syncwarp();
       const uint32_t bytes = meta[0];
       if (!(bytes & kNone)) {
+        if (__any_sync(~0u, !mbar_wait(&sh.full[warp][st], parity >> st & 1, late))) late = true;
+        parity ^= 1u << st;
         const uint8_t* kc = ring + st * 2 * C::HALF;
-        const uint8_t* vc = kc + C::HALF;
         // scores of keys gid and gid + 8
         float x[NB][4];
 #pragma unroll
@@ -265,44 +258,54 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
           for (int z = 0; z < 4; ++z) x[nb][z] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 64; ++k) {
-          const uint4 p = *reinterpret_cast<const uint4*>(kc + place_k<D>(gid, k * 4 + t4));
-          const uint4 q = *reinterpret_cast<const uint4*>(kc + place_k<D>(gid + 8, k * 4 + t4));
+          const uint4 p = *reinterpret_cast<const uint4*>(kc + k_at[k]);
+          const uint4 q = *reinterpret_cast<const uint4*>(kc + kOn + k_at[k]);
           const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const uint32_t a0 = lo2(pw[w]), a1 = lo2(qw[w]), a2 = hi2(pw[w]), a3 = hi2(qw[w]);
+            uint32_t a0, a1, a2, a3;
+            halves(pw[w], a0, a2);
+            halves(qw[w], a1, a3);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) mma(x[nb], a0, a1, a2, a3, qf[nb][k * 4 + w][0], qf[nb][k * 4 + w][1]);
           }
         }
-        const int ek = (int)(bytes & 255u), ev = (int)(bytes >> 8 & 255u);
-        const float shift = ev == 255 ? CUDART_NAN_F : (float)(ev - 127);
+        const uint32_t ek = bytes & 255u, ev = bytes >> 8 & 255u;
+        const float kf = scale_of(ek), shift = ev == 255u ? 0.f : (float)((int)ev - 127);
         const bool special = key0 + kChunk > r.ctx;  // new keys, or rows past the end
         uint32_t seen[NB][2];                        // the row's keys of the chunk
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = ek == 255 ? CUDART_NAN_F : power(ek - 127 - re[nb][j]);
+            const float f = ek == 255u ? kf : fminf(kf * rf[nb][j], 3e38f);
             x[nb][j] *= f;
             x[nb][2 + j] *= f;
-            seen[nb][j] = ~0u;
-            if (special) {
-              const int off = key0 - r.ctx;
-              seen[nb][j] = off < 0 ? vis[nb][j] << -off | ((1u << -off) - 1) : off < 32 ? vis[nb][j] >> off : 0u;
+          }
+        }
+        if (special) {
+          const int off = key0 - r.ctx;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              seen[nb][j] = off < 0 ? vis[nb][j] << -off | ((1u << -off) - 1) : vis[nb][j] >> off;
               if (nb * 8 + 2 * t4 + j >= rows) seen[nb][j] = 0;
               if (!(seen[nb][j] >> gid & 1)) x[nb][j] = -CUDART_INF_F;
               if (!(seen[nb][j] >> (gid + 8) & 1)) x[nb][2 + j] = -CUDART_INF_F;
             }
           }
         }
+        float y[NB][4];
         bool grow = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          // (before a row's first key mo is -inf, and any score is above)
+          const float most[2] = {fminf(kLagL, mo[nb][0] + (kLagP - shift)), fminf(kLagL, mo[nb][1] + (kLagP - shift))};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const float m = M[nb][z & 1], y = (x[nb][z] - m) * g.c;
-            grow |= x[nb][z] > -CUDART_INF_F && (m == -CUDART_INF_F || y > kLagL || y + shift - mo[nb][z & 1] > kLagP);
+            y[nb][z] = (x[nb][z] - Mr[nb][z & 1]) * g.c;
+            grow |= y[nb][z] > most[z & 1];
           }
         }
         if (__any_sync(~0u, grow)) {
@@ -319,12 +322,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
                 const float down = was == -CUDART_INF_F ? 0.f : (was - m) * g.c;
                 const float before = mo[nb][j] + down, now = fmaxf(before, (top - m) * g.c + shift);
                 const float f = before == -CUDART_INF_F ? 1.f : ex2(before - now);
-                M[nb][j] = m;
+                M[nb][j] = Mr[nb][j] = m;
                 mo[nb][j] = now;
+                up[nb][j] = kUp - (now == -CUDART_INF_F ? 0.f : now);
                 l[nb][j] *= ex2(down);
 #pragma unroll
                 for (int k = 0; k < MT; ++k) o[k][nb][j] *= f, o[k][nb][2 + j] *= f;
               }
+              y[nb][j] = (x[nb][j] - Mr[nb][j]) * g.c;
+              y[nb][2 + j] = (x[nb][2 + j] - Mr[nb][j]) * g.c;
             }
           }
         }
@@ -334,12 +340,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
           float w[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int j = z & 1;
-            const float m = M[nb][j] == -CUDART_INF_F ? 0.f : M[nb][j], off = mo[nb][j] == -CUDART_INF_F ? 0.f : mo[nb][j];
-            const float y = (x[nb][z] - m) * g.c;
-            l[nb][j] += ex2(y);
+            l[nb][z & 1] += ex2(y[nb][z]);
             // 16 bits are what the product takes; the sum keeps all 32
-            w[z] = x[nb][z] == -CUDART_INF_F ? 0.f : ex2(y + (shift - off + kUp));
+            w[z] = ex2(y[nb][z] + (shift + up[nb][z & 1]));
+          }
+          if (ev == 255u) {  // NaN to the rows that see the key
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[z] = x[nb][z] == -CUDART_INF_F ? 0.f : CUDART_NAN_F;
           }
           pf[nb][0] = transpose8(Elem<__half>::pack(w[0], w[1]));
           pf[nb][1] = transpose8(Elem<__half>::pack(w[2], w[3]));
@@ -348,12 +355,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-          const int row = 2 * t4 + (z & 1) + (z >> 1) * 8;
+          const uint8_t* from = kc + (z < 2 ? 0 : kOn) + v_at[z & 1];
           if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(vc + place_v<D>(row, gid));
+            const uint4 u = *reinterpret_cast<const uint4*>(from);
             v[z][0] = u.x, v[z][1] = u.y, v[z][2] = u.z, v[z][3] = u.w;
           } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(vc + place_v<D>(row, gid >> 1) + (gid & 1) * 8);
+            const uint2 u = *reinterpret_cast<const uint2*>(from);
             v[z][0] = u.x, v[z][1] = u.y;
           }
         }
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
 #pragma unroll
               for (int b = 0; b < D / 8; ++b) {
                 const int d = gid * (D / 8) + b;
-                if ((vc[place_v<D>(key, d >> 4) + (d & 15)] & 0x7F) != 0x7F) continue;
+                if ((kc[C::HALF + place<D>(key, d >> 4) + (d & 15)] & 0x7F) != 0x7F) continue;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -389,7 +396,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
         for (int w = 0; w < D / 32; ++w) {
           const uint32_t p0 = __byte_perm(v[0][w], v[1][w], 0x5140), p1 = __byte_perm(v[0][w], v[1][w], 0x7362);
           const uint32_t q0 = __byte_perm(v[2][w], v[3][w], 0x5140), q1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-          const uint32_t f0[4] = {lo2(p0), hi2(p0), lo2(q0), hi2(q0)}, f1[4] = {lo2(p1), hi2(p1), lo2(q1), hi2(q1)};
+          uint32_t f0[4], f1[4];
+          halves(p0, f0[0], f0[1]);
+          halves(q0, f0[2], f0[3]);
+          halves(p1, f1[0], f1[1]);
+          halves(q1, f1[2], f1[3]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             mma(o[2 * w][nb], f0[0], f0[1], f0[2], f0[3], pf[nb][0], pf[nb][1]);
@@ -397,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
           }
         }
       }
+      proxy_fence_reads();
       __syncwarp();
       const int after = page_of(t + S + 1);
       const uint32_t next = issue(t + S, st, page);
@@ -406,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
       meta[S - 1] = next;
       if (++st == S) st = 0;
     }
-    copy_wait<0>();
 
     // The warps' sums joined: in the rings' place, [warp][number of a lane][gid][row].
 #pragma unroll
@@ -497,17 +508,40 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
         g.cut[blockIdx.x] = Cut{deal.owner(it) - (int)blockIdx.x + 1, rows, r.q0, wk.h};
       }
     }
-    __syncthreads();  // the outputs have been read
+    proxy_fence_reads();
+    late = __syncthreads_or(late);  // the outputs have been read
   }
   if (tid == 0 && !has_cut) g.cut[blockIdx.x].parts = 0;
+  if (late) {
+    // Every copy has been waited for unless a wait ran out; those still in flight get kDrainNs.
+    for (const uint64_t t0 = global_ns(); global_ns() - t0 < tree_attention::kDrainNs;) __nanosleep(1000);
+    if (tid == 0 && a.status) atomicOr(a.status, FT_ST_TIMEOUT);
+  }
+}
+
+// (L2 fetches a row and no more: the head beside it is another CTA's, and with 256 bytes 64 requests of 16384 keys took
+// 244 us in place of 177)
+inline bool chunk_map(CUtensorMap* map, void* base, const ft_kv_cache& c, int64_t page, int64_t token, int64_t head, char* msg,
+                      size_t len) {
+  const uint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.page_size, (uint64_t)c.kv_heads, (uint64_t)c.num_pages};
+  const uint64_t strides[3] = {(uint64_t)token, (uint64_t)(c.kv_heads > 1 ? head : c.head_dim),
+                               (uint64_t)(c.num_pages > 1 ? page : c.head_dim)};
+  const uint32_t box[4] = {(uint32_t)c.head_dim, kChunk, 1, 1};
+  return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, msg, len, c.head_dim, c.head_dim);
 }
 
 template <typename E, int D, int NB>
 int launch(const Args& g, int grid, cudaStream_t st) {
   using C = Cfg<D, NB>;
-  constexpr int smem = C::SMEM + (int)sizeof(Shared<C::R>);
+  constexpr int smem = C::SMEM + (int)sizeof(Shared<C::R, C::STAGES>);
   static_assert(smem * C::CTAS <= 227 * 1024, "the CTAs of an SM must fit its shared memory");
   static_assert(Held<__half>::kUp == 11.f && Held<__nv_bfloat16>::kUp == 0.f, "parts' sums are scaled by 2^kUp");
+  const ft_kv_cache& c = g.a.cache;
+  CUtensorMap mk, mv;
+  char msg[128] = "";
+  if (!chunk_map(&mk, c.k, c, c.k_page_stride, c.k_token_stride, c.k_head_stride, msg, sizeof(msg)) ||
+      !chunk_map(&mv, c.v, c, c.v_page_stride, c.v_token_stride, c.v_head_stride, msg, sizeof(msg)))
+    return record_error(FT_E_CUDA, "%s", msg);
   static thread_local int configured = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -519,7 +553,7 @@ int launch(const Args& g, int grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   pdl_config(cfg, attr, dim3(grid), dim3(kThreads), smem, st);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<E, D, NB>, g);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, few_rows_kernel<E, D, NB>, mk, mv, g);
   if (e == cudaSuccess) e = tree_attention::launch_join<E, D, kRows>(g, grid, st);
   if (e != cudaSuccess) return record_error(FT_E_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
   return FT_OK;

@@ -183,7 +183,7 @@ bool make_weight_maps(PrefillState* p, int b, char* msg, size_t n) {
     const uint64_t dims[4] = {d, f, 2, E};
     const uint64_t strides[3] = {d * 2, d * f * 2, Bx};
     const uint32_t box[4] = {64, 128, 1, 1};
-    if (!encode_tensor_map(&p->map_w1[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, lb, dims, strides, box, msg, n, true))
+    if (!encode_tensor_map(&p->map_w1[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, lb, dims, strides, box, msg, n, 128))
       return false;
   }
   {
@@ -191,7 +191,7 @@ bool make_weight_maps(PrefillState* p, int b, char* msg, size_t n) {
     const uint64_t strides[2] = {f * 2, Bx};
     const uint32_t box[3] = {64, 256, 1};
     if (!encode_tensor_map(&p->map_w2[b], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, lb + 4 * d * f, dims, strides, box, msg,
-                           n, true))
+                           n, 128))
       return false;
   }
   return true;
@@ -297,28 +297,28 @@ PrefillState* prefill_create(const PrefillConfig& cfg, char* msg, size_t msg_len
     const uint64_t dims[2] = {(uint64_t)cfg.d, (uint64_t)p->rows_cap};
     const uint64_t strides[1] = {(uint64_t)cfg.d * 2};
     const uint32_t box[2] = {64, 128};
-    ok = encode_tensor_map(&p->map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p->xs, dims, strides, box, msg, msg_len, true);
+    ok = encode_tensor_map(&p->map_x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p->xs, dims, strides, box, msg, msg_len, 128);
   }
   if (ok) {
     const uint64_t dims[2] = {(uint64_t)cfg.f, (uint64_t)p->rows_cap};
     const uint64_t strides[1] = {(uint64_t)cfg.f * 2};
     const uint32_t box[2] = {64, 128};
     ok = encode_tensor_map(&p->map_h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p->hbuf, dims, strides, box, msg, msg_len,
-                           true);
+                           128);
   }
   if (ok) {
     const uint64_t dims[2] = {(uint64_t)cfg.f, (uint64_t)p->rows_cap};
     const uint64_t strides[1] = {(uint64_t)cfg.f * 2};
     const uint32_t box[2] = {64, 32};
     ok = encode_tensor_map(&p->map_h_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p->hbuf, dims, strides, box, msg,
-                           msg_len, true);
+                           msg_len, 128);
   }
   if (ok) {
     const uint64_t dims[2] = {(uint64_t)cfg.d, (uint64_t)p->rows_cap};
     const uint64_t strides[1] = {(uint64_t)cfg.d * 4};
     const uint32_t box[2] = {32, 32};
     ok = encode_tensor_map(&p->map_y_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, p->ybuf, dims, strides, box, msg,
-                           msg_len, true);
+                           msg_len, 128);
   }
   if (!ok) {
     prefill_destroy(p);

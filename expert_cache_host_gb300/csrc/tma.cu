@@ -25,7 +25,7 @@ EncodeFn encoder() {
 
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, void* base, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box, char* msg, size_t msg_len,
-                       bool swizzle128) {
+                       int swizzle, int l2_bytes) {
   EncodeFn fn = encoder();
   if (!fn) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
@@ -40,7 +40,10 @@ bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t ran
     if (i + 1 < rank) gs[i] = strides_bytes[i];
   }
   CUresult r = fn(map, dtype, rank, base, gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  l2_bytes == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                  : l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                    : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(msg, msg_len, "cuTensorMapEncodeTiled failed with %d", (int)r);

@@ -145,9 +145,10 @@ __device__ __forceinline__ void tensor_g2s_4d(void* dst, const CUtensorMap* map,
 }
 
 // Host: encode a tiled tensor map (returns false if the driver refuses it).
-// swizzle128 selects the 128-byte swizzle layout (inner box extent must then be 128 bytes).
+// swizzle: 128 or 64 selects the swizzle layout of so many bytes (which the inner box extent must then be).
+// l2_bytes: what L2 fetches where some of it misses, 256, 128 or 64.
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, void* base, const uint64_t* dims,
                        const uint64_t* strides_bytes, const uint32_t* box, char* msg, size_t msg_len,
-                       bool swizzle128 = false);
+                       int swizzle = 0, int l2_bytes = 256);
 
 }  // namespace ft

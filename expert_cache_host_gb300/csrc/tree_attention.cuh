@@ -1156,9 +1156,9 @@ bool cache_map(CUtensorMap* map, void* base, const ft_kv_cache& c, int64_t page,
   const uint64_t strides[3] = {(uint64_t)token * size, (uint64_t)(c.kv_heads > 1 ? head : c.head_dim) * size,
                                (uint64_t)(c.num_pages > 1 ? page : c.head_dim) * size};
   const uint32_t box[4] = {Q8 ? (uint32_t)c.head_dim : 64, (uint32_t)(c.page_size < KT ? c.page_size : KT), 1, 1};
-  if (Q8) return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, msg, len);
+  if (Q8) return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, msg, len, 0, c.head_dim);
   return encode_tensor_map(map, c.dtype == FT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                           4, base, dims, strides, box, msg, len, true);
+                           4, base, dims, strides, box, msg, len, 128);
 }
 
 template <typename E, int D, int ROWS>
@@ -1183,7 +1183,7 @@ int launch(const Args& g, int grid, cudaStream_t st) {
   const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)(a.max_tokens > 1 ? a.q_stride : (int64_t)a.q_heads * D) * 2};
   const uint32_t box[3] = {64, (uint32_t)g.G, (uint32_t)g.tpt};
   if (!encode_tensor_map(&mq, Elem<E>::kDtype == FT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                         3, const_cast<void*>(a.q), dims, strides, box, msg, sizeof(msg), true) ||
+                         3, const_cast<void*>(a.q), dims, strides, box, msg, sizeof(msg), 128) ||
       !cache_map<Q8>(&mk, c.k, c, c.k_page_stride, c.k_token_stride, c.k_head_stride, msg, sizeof(msg)) ||
       !cache_map<Q8>(&mv, c.v, c, c.v_page_stride, c.v_token_stride, c.v_head_stride, msg, sizeof(msg)))
     return record_error(FT_E_CUDA, "%s", msg);

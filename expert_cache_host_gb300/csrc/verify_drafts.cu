@@ -9,15 +9,19 @@
 // One row of either kind and request is what the call cannot do without, HBM
 // bounds large batches, latency a single request.
 //
-// The token is a whole number next to borders of the running sum, so sums are
-// 64-bit fixed point (units of 2^-59, entries up to 2): exact in any order, where
-// fp32 sums over 131072 entries would move the borders by more than many entries
-// are wide, and 64-bit floating point runs at a sixty-fourth of the rate.  a is
-// never stored: it follows from p, q and the few A's before it.
+// The token is a whole number next to borders of the running sum: fp32 sums over
+// 131072 entries would move the borders by more than many entries are wide, and
+// 64-bit floating point runs at a sixty-fourth of the rate.  So entries are cut into
+// whole numbers at three levels (multiples of 2^-22, 2^-40 and 2^-59; adding a
+// constant leaves each level's number in the sum's low bits) and added as such:
+// sums do not depend on their order.  After k rejections
+//   a = max(p - q B, 0),  B = 1 + A_1 + .. + A_(k-1)
+// (what one step cuts off at 0 the next ones would take below it), so a is never
+// stored and takes one product, in two fp32 numbers: exact to 2^-46.
 //
 // A cluster of CTAs shares a request.  CTA 0 walks and says what the cluster
-// does next; every warp sums one stretch of the row, and the stretch that holds
-// the drawn point is gone through once more.
+// does next; every warp sums one stretch of the row and keeps its pieces' sums,
+// and the piece that holds the drawn point is gone through once more.
 #include <cooperative_groups.h>
 
 #include "attn_side.h"
@@ -32,9 +36,9 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kNodes = 512;  // rows of a request whose entries are gathered ahead
 constexpr int kRejected = 64;
-constexpr int kUnit = 59;  // fixed point: units of 2^-59
-constexpr uint64_t kOne = 1ull << kUnit;
+constexpr int kUnit = 59;  // sums are in units of 2^-59
 constexpr int kBatch = 4;  // vectors a lane loads before it uses the first
+constexpr int kPieces = 64;  // of a warp's stretch
 
 template <typename E>
 struct Prob {  // a 16-byte vector of a row
@@ -63,17 +67,29 @@ struct Prob<float> {
 __device__ __forceinline__ bool in_range(float v) { return v >= 0.f && v <= 2.f; }
 // A random number as it is used.
 __device__ __forceinline__ float below_one(float u) { return u > 0.f ? fminf(u, 0.99999994f) : 0.f; }
-// v in [0, 2] in units of 2^-59, cut off below them.
-__device__ __forceinline__ uint64_t fixed(float v) {
-  const uint32_t bits = __float_as_uint(v) & 0x7FFFFFFFu;  // (-0 is 0)
-  const int e = (int)(bits >> 23);
-  // the significand at bits 37 .. 60 stands for e = 128
-  const uint64_t m = (uint64_t)((bits & 0x7FFFFFu) | (e ? 0x800000u : 0u)) << 37;
-  return m >> min(128 - e, 63);
-}
-__device__ __forceinline__ uint64_t times(uint64_t q, uint64_t A) {  // q A in units of 2^-59
-  return __umul64hi(q, A) << (64 - kUnit) | (q * A) >> kUnit;
-}
+
+// Sums of numbers hi + lo in [0, 2] (|lo| <= 2^-24 hi) as whole numbers at three
+// levels; each counts the constants' bits once a number.
+struct Levels {
+  uint32_t a = 0, b = 0, c = 0;
+  static constexpr float kA = 2.f, kB = 0x1.8p-17f, kC = 0x1.8p-36f;
+  __device__ __forceinline__ void add(float hi, float lo) {
+    const float s = hi + kA, r = (hi - (s - kA)) + lo;
+    const float t = r + kB, q = r - (t - kB);
+    a += __float_as_uint(s);
+    b += __float_as_uint(t);
+    c += __float_as_uint(q + kC);
+  }
+  // What `n` numbers gave, without the constants.
+  __device__ __forceinline__ void finish(uint32_t n) {
+    a -= n * __float_as_uint(kA);
+    b -= n * __float_as_uint(kB);
+    c -= n * __float_as_uint(kC);
+  }
+  __device__ __forceinline__ uint64_t value() const {
+    return ((uint64_t)a << (kUnit - 22)) + ((int64_t)(int32_t)b << (kUnit - 40)) + (int64_t)(int32_t)c;
+  }
+};
 
 struct Node {
   int parent, token;
@@ -85,10 +101,11 @@ enum Command : int { kSum, kDraw };
 struct Shared {
   Node nodes[kNodes];
   // what CTA 0 says
-  int command, row, k;           // the row that is read (in the batch), rejections so far
-  uint64_t mass[kRejected + 1];  // A before each rejection
-  int gone[kRejected];           // rejected tokens
-  // sums of a pass: of this CTA's warps, of all CTAs
+  int command, row, k;  // the row that is read (in the batch), rejections so far
+  float b_hi, b_lo;     // B
+  int gone[kRejected];  // rejected tokens
+  // sums of a pass: of a warp's pieces, of this CTA's warps, of all CTAs
+  uint64_t piece[kWarps][kPieces];
   uint64_t warp_sum[kWarps], cta_sum[kMaxCluster];
   float warp_size[kWarps], cta_size[kMaxCluster];
 };
@@ -132,24 +149,22 @@ __device__ __forceinline__ uint4 load(const void* row, bool vec, int first, int 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// a of a group's elements.
+// What is left of a group's elements, as hi + lo.
 template <typename E>
 struct Weights {
-  uint64_t a[Prob<E>::N];
-  float size;  // sum of p, roughly
+  float hi[Prob<E>::N], lo[Prob<E>::N];
   bool bad;
-  __device__ __forceinline__ void make(const Shared& sh, const uint4& vp, const uint4& vq, bool draft, int first, int k) {
+  __device__ __forceinline__ void make(const Shared& sh, const uint4& vp, const uint4& vq, bool draft, int first, int k,
+                                       float b_hi, float b_lo) {
     constexpr int N = Prob<E>::N;
-    float p[N];
-    Prob<E>::all(vp, p);
+    Prob<E>::all(vp, hi);
     bad = false;
-    size = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool ok = in_range(p[i]);
+      const bool ok = in_range(hi[i]);
       bad |= !ok;
-      size += ok ? p[i] : 0.f;
-      a[i] = ok ? fixed(p[i]) : 0;
+      hi[i] = ok ? hi[i] : 0.f;
+      lo[i] = 0.f;
     }
     if (k == 0) return;
     if (!draft) {
@@ -157,7 +172,7 @@ struct Weights {
         const uint32_t at = (uint32_t)(sh.gone[j] - first);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (at == (uint32_t)i) a[i] = 0;
+          if (at == (uint32_t)i) hi[i] = 0.f;
       }
       return;
     }
@@ -167,12 +182,13 @@ struct Weights {
     for (int i = 0; i < N; ++i) {
       const bool ok = in_range(q[i]);
       bad |= !ok;
-      const uint64_t f = ok ? fixed(q[i]) : 0;
-      a[i] = a[i] > f ? a[i] - f : 0;  // A = 1 before the first rejection
-      for (int j = 1; j < k; ++j) {
-        const uint64_t less = times(f, sh.mass[j]);
-        a[i] = a[i] > less ? a[i] - less : 0;
-      }
+      const float f = ok ? q[i] : 0.f;
+      const float t = f * b_hi, e = fmaf(f, b_lo, fmaf(f, b_hi, -t));  // f B = t + e
+      const float d = hi[i] - t, v = d - hi[i];
+      const float l = ((hi[i] - (d - v)) - (t + v)) - e;  // hi - t = d + the first difference, exactly
+      const bool some = d + l > 0.f;
+      hi[i] = some ? d : 0.f;
+      lo[i] = some ? l : 0.f;
     }
   }
 };
@@ -187,11 +203,12 @@ __device__ __forceinline__ T warp_sum(T x) {
 // The walk's state, in CTA 0's first warp (every lane the same).
 struct Walk {
   int at, last, k, count;  // row reached, last child tried, rejections at `at`, accepted rows
-  bool summed;             // the sums of a pass are those of (at, k)
+  bool known;              // A after k rejections is
+  double A, B;             // it, and those before it together
 };
 
 template <typename E, int CS>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_constant__ ft_verify_args a) {
+__global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ ft_verify_args a) {
   __shared__ Shared sh;
   pdl_wait();
   pdl_trigger();
@@ -234,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
     __syncthreads();
   }
   if constexpr (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
-  Walk w{0, 0, 0, 0, false};
+  Walk w{0, 0, 0, 0, true, 1.0, 0.0};
   bool bad = false, bad_token = false, bad_tree = false;
   for (;;) {
     if (rank == 0 && warp == 0) {
@@ -265,48 +282,31 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
           w.last = child;
           continue;
         }
-        // A after k rejections
-        if (w.k > 0 && !w.summed) {
+        if (!w.known) {
           command = kSum;
           break;
         }
         const bool ok_p = in_range(x.p), ok_q = in_range(x.q);
         bad |= !ok_p || !ok_q;
-        const float p = ok_p ? x.p : 0.f, q = ok_q ? x.q : 0.f;
-        const float u = below_one(x.u);
-        bool yes;
-        uint64_t ax = fixed(p);
-        if (w.k == 0) {
-          yes = (double)u * (double)q < (double)p;  // (the product is exact)
+        const double p = ok_p ? x.p : 0.f, q = ok_q ? x.q : 0.f, u = below_one(x.u);
+        double left = p;
+        if (a.draft_probs) {
+          left = fmax(p - q * w.B, 0.0);
         } else {
-          if (a.draft_probs) {
-            const uint64_t f = fixed(q);
-            for (int j = 0; j < w.k; ++j) {
-              const uint64_t less = times(f, sh.mass[j]);
-              ax = ax > less ? ax - less : 0;
-            }
-          } else {
-            for (int j = 0; j < w.k; ++j)
-              if (sh.gone[j] == x.token) ax = 0;
-          }
-          yes = (double)u * (double)q * (double)sh.mass[w.k] < (double)ax;
+          for (int j = 0; j < w.k; ++j)
+            if (sh.gone[j] == x.token) left = 0.0;
         }
         w.last = child;
-        if (yes) {
+        if (u * q * w.A < left) {  // (exact before the first rejection: two fp32 numbers' product)
           if (lane == 0) a.accepted[q0 + w.count] = child;
-          ++w.count;
-          w.at = child;
-          w.k = 0;
-          w.summed = false;
+          w = Walk{child, child, 0, w.count + 1, true, 1.0, 0.0};
         } else {
-          if (lane == 0) {
-            sh.gone[w.k] = x.token;
-            if (w.k == 0) sh.mass[0] = kOne;
-            if (!a.draft_probs && w.summed) sh.mass[w.k + 1] = sh.mass[w.k] - ax;
-          }
+          if (lane == 0) sh.gone[w.k] = x.token;
           __syncwarp();
-          // without draft probabilities the next A is known; the stretches' sums are not
-          w.summed = w.summed && !a.draft_probs;
+          w.B += w.A;
+          // without draft probabilities the next A is known once one sum is
+          w.known = w.k > 0 && !a.draft_probs;
+          if (w.known) w.A -= left;
           ++w.k;
         }
       }
@@ -316,10 +316,9 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
         to->command = command;
         to->row = w.at;
         to->k = w.k;
-        for (int j = 0; j < w.k; ++j) {
-          to->gone[j] = sh.gone[j];
-          to->mass[j] = sh.mass[j];
-        }
+        to->b_hi = (float)w.B;
+        to->b_lo = (float)(w.B - (double)(float)w.B);
+        for (int j = 0; j < w.k; ++j) to->gone[j] = sh.gone[j];
       }
     }
     everyone();
@@ -331,12 +330,15 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
     const int g0 = (rank * kWarps + warp) * per, g1 = min(g0 + per, r.groups);
     const bool vec = r.off >= 0;
     const int base = (vec ? r.off : 0) - N;  // first element of group 0
+    // A stretch is gone through kBatch vectors a lane at a time; a piece is one such step, or several of a long one.
+    const int steps = (per + 32 * kBatch - 1) / (32 * kBatch), to_piece = (steps + kPieces - 1) / kPieces;
+    const float b_hi = sh.b_hi, b_lo = sh.b_lo;
     uint64_t total = 0;
     for (;;) {
-      // the stretch's sum
-      uint64_t sum = 0;
+      uint64_t sum = 0, piece = 0;
       float size = 0.f;
-      for (int g = g0 + lane; g < g1; g += 32 * kBatch) {
+      for (int step = 0; step < steps; ++step) {
+        const int g = g0 + step * 32 * kBatch + lane;
         uint4 vp[kBatch], vq[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -347,18 +349,27 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
             if (r.q && k > 0) vq[i] = load<E>(r.q, vec, first, a.V);
           }
         }
+        Levels s;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           Weights<E> x;
-          x.make(sh, vp[i], vq[i], r.q != nullptr, base + (g + 32 * i) * N, k);
+          x.make(sh, vp[i], vq[i], r.q != nullptr, base + (g + 32 * i) * N, k, b_hi, b_lo);
           bad |= x.bad;
-          size += x.size;
 #pragma unroll
-          for (int j = 0; j < N; ++j) sum += x.a[j];
+          for (int j = 0; j < N; ++j) s.add(x.hi[j], x.lo[j]);
+        }
+        s.finish(kBatch * N);
+        // (the first level's number in two parts: a warp's could pass 32 bits)
+        const uint32_t up = __reduce_add_sync(~0u, s.a >> 12), low = __reduce_add_sync(~0u, s.a & 0xFFFu);
+        const int32_t b32 = __reduce_add_sync(~0u, (int32_t)s.b), c32 = __reduce_add_sync(~0u, (int32_t)s.c);
+        piece += (((uint64_t)up << 12) + low << (kUnit - 22)) + ((int64_t)b32 << (kUnit - 40)) + (int64_t)c32;
+        size += (float)up * 0x1p-10f;
+        if (step + 1 == steps || (step + 1) % to_piece == 0) {
+          if (lane == 0) sh.piece[warp][step / to_piece] = piece;
+          sum += piece;
+          piece = 0;
         }
       }
-      sum = warp_sum(sum);
-      size = warp_sum(size);
       if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_size[warp] = size;
       __syncthreads();
       if (tid < CS) {
@@ -383,9 +394,8 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
     }
     if (command == kSum) {
       if (rank == 0 && warp == 0) {
-        if (lane == 0) sh.mass[w.k] = total;
-        __syncwarp();
-        w.summed = true;
+        w.A = (double)total * 0x1p-59;
+        w.known = true;
       }
       everyone();  // (the sums have been read)
       continue;
@@ -412,39 +422,62 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const __grid_co
           left -= sh.warp_sum[i];
         }
         if (left != ~0ull && left < sh.warp_sum[warp]) {  // this warp's stretch holds the point
-          for (int gg = g0; gg < g1; gg += 32) {
-            const int g = gg + lane, first = base + g * N;
-            uint4 vp = make_uint4(0, 0, 0, 0), vq = vp;
-            if (g < g1) {
-              vp = load<E>(r.p, vec, first, a.V);
-              if (r.q && k > 0) vq = load<E>(r.q, vec, first, a.V);
-            }
-            Weights<E> x;
-            x.make(sh, vp, vq, r.q != nullptr, first, k);
-            uint64_t mine = 0;
+          int step = 0;
+          for (int at = 0; left >= sh.piece[warp][at]; ++at) {  // (their sum is above it)
+            left -= sh.piece[warp][at];
+            step += to_piece;
+          }
+          bool found = false;
+          for (; step < steps && !found; ++step) {
+            const int gg = g0 + step * 32 * kBatch + lane;
+            uint4 vp[kBatch], vq[kBatch];
 #pragma unroll
-            for (int j = 0; j < N; ++j) mine += x.a[j];
-            uint64_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const uint64_t y = __shfl_up_sync(~0u, upto, o);
-              if (lane >= o) upto += y;
-            }
-            const uint32_t hit = __ballot_sync(~0u, upto > left);
-            if (hit) {
-              if (lane == __ffs(hit) - 1) {
-                uint64_t c = upto - mine;
-                int token = -1;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                  c += x.a[j];
-                  if (token < 0 && c > left) token = first + j;
-                }
-                a.next_token[b] = token;
+            for (int i = 0; i < kBatch; ++i) {
+              const int first = base + (gg + 32 * i) * N;
+              vp[i] = vq[i] = make_uint4(0, 0, 0, 0);
+              if (gg + 32 * i < g1) {
+                vp[i] = load<E>(r.p, vec, first, a.V);
+                if (r.q && k > 0) vq[i] = load<E>(r.q, vec, first, a.V);
               }
-              break;
             }
-            left -= __shfl_sync(~0u, upto, 31);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              if (found) break;
+              const int first = base + (gg + 32 * i) * N;
+              Weights<E> x;
+              x.make(sh, vp[i], vq[i], r.q != nullptr, first, k, b_hi, b_lo);
+              auto value = [&](int j) {
+                Levels s;
+                s.add(x.hi[j], x.lo[j]);
+                s.finish(1);
+                return s.value();
+              };
+              uint64_t mine = 0;
+#pragma unroll
+              for (int j = 0; j < N; ++j) mine += value(j);
+              uint64_t upto = mine;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t y = __shfl_up_sync(~0u, upto, o);
+                if (lane >= o) upto += y;
+              }
+              const uint32_t hit = __ballot_sync(~0u, upto > left);
+              if (hit) {
+                if (lane == __ffs(hit) - 1) {
+                  uint64_t c = upto - mine;
+                  int token = -1;
+#pragma unroll
+                  for (int j = 0; j < N; ++j) {
+                    c += value(j);
+                    if (token < 0 && c > left) token = first + j;
+                  }
+                  a.next_token[b] = token;
+                }
+                found = true;
+              } else {
+                left -= __shfl_sync(~0u, upto, 31);
+              }
+            }
           }
         }
       }

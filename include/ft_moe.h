@@ -770,10 +770,12 @@ int ft_kv8_attention_workspace(const ft_kv8_attn_args* args, uint64_t* bytes);
  *   accepted   [max_tokens] the request's accepted rows in order, from
  *              accepted[q_start[b]] on, then -1
  *   n_accepted [num_reqs], next_token [num_reqs]
- * Rows whose parent is no row of theirs take no part.  Sums are exact to 2^-59 an
- * entry (64-bit fixed point), so results do not depend on any order.  An entry
+ * Rows whose parent is no row of theirs take no part.  Sums are of whole
+ * numbers, entries exact to 2^-59 (after a rejection 2^-46), so results do not
+ * depend on any order.  An entry
  * outside [0, 2] counts as 0; it is reported (FT_ST_NAN) where it is met, and so is
- * a row with nothing to draw from or a sum above 8: next_token is -1 there.  A
+ * a row with nothing to draw from or a sum above 8 of what is drawn from: next_token
+ * is -1 there.  A
  * drafted token outside [0, V) is reported (FT_ST_BAD_TOKEN) and takes no part; so
  * does, reported as FT_ST_BAD_TREE, any child after the 64th that a row rejects.  A
  * request without rows gets 0 and -1.  Rows at or past q_start[num_reqs] are not

@@ -19,9 +19,13 @@
 // (what one step cuts off at 0 the next ones would take below it), so a is never
 // stored and takes one product, in two fp32 numbers: exact to 2^-46.
 //
-// A cluster of CTAs shares a request.  CTA 0 walks and says what the cluster
-// does next; every warp sums one stretch of the row and keeps its pieces' sums,
-// and the piece that holds the drawn point is gone through once more.
+// A cluster of CTAs shares a request.  CTA 0 walks, a row of the request a lane,
+// and says what the cluster does next; every warp sums one stretch of the row and
+// keeps its pieces' sums, and the piece that holds the drawn point is gone through
+// once more, by the same loop.  Vectors come through shared memory (a thread's own,
+// kDepth ahead), so that the loop stays rolled: one request is bound by latency, and
+// with four vectors' arithmetic unrolled twice most of it was the instructions'
+// (15000 cycles for a row's eighth, first time through).
 #include <cooperative_groups.h>
 
 #include "attn_side.h"
@@ -34,11 +38,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kNodes = 512;  // rows of a request whose entries are gathered ahead
 constexpr int kRejected = 64;
 constexpr int kUnit = 59;  // sums are in units of 2^-59
-constexpr int kBatch = 4;  // vectors a lane loads before it uses the first
-constexpr int kPieces = 64;  // of a warp's stretch
+constexpr int kDepth = 8;     // vectors of a thread on their way
+constexpr int kPieces = 64;   // of a warp's stretch at most
+constexpr int kPiece = 4;     // vectors a lane of a piece, or a multiple
+constexpr int kResident = 2;  // CTAs of an SM
 
 template <typename E>
 struct Prob {  // a 16-byte vector of a row
@@ -91,15 +96,10 @@ struct Levels {
   }
 };
 
-struct Node {
-  int parent, token;
-  float u, p, q;
-};
-
 enum Command : int { kSum, kDraw };
 
 struct Shared {
-  Node nodes[kNodes];
+  uint4 ring[kDepth][2][kThreads];
   // what CTA 0 says
   int command, row, k;  // the row that is read (in the batch), rejections so far
   float b_hi, b_lo;     // B
@@ -131,12 +131,10 @@ __device__ __forceinline__ Row row_at(const ft_verify_args& a, int64_t t) {
   return r;
 }
 
-// Group g of a row: elements first(g) .. + N - 1, those outside [0, V) as 0.
+// Elements first .. first + N - 1 of a row, those outside [0, V) as 0.
 template <typename E>
-__device__ __forceinline__ uint4 load(const void* row, bool vec, int first, int V) {
+__device__ __noinline__ uint4 load_edge(const void* row, int first, int V) {
   constexpr int N = Prob<E>::N;
-  if (vec && first >= 0 && first + N <= V)
-    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (int64_t)first * (16 / N)));
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -149,55 +147,35 @@ __device__ __forceinline__ uint4 load(const void* row, bool vec, int first, int 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// What is left of a group's elements, as hi + lo.
+// A vector's numbers; those outside [0, 2] become 0, and whether there are any.
 template <typename E>
-struct Weights {
-  float hi[Prob<E>::N], lo[Prob<E>::N];
-  bool bad;
-  __device__ __forceinline__ void make(const Shared& sh, const uint4& vp, const uint4& vq, bool draft, int first, int k,
-                                       float b_hi, float b_lo) {
-    constexpr int N = Prob<E>::N;
-    Prob<E>::all(vp, hi);
-    bad = false;
+__device__ __forceinline__ bool numbers(const uint4& v, float* f) {
+  constexpr int N = Prob<E>::N;
+  Prob<E>::all(v, f);
+  uint32_t most = 0;  // (as whole numbers: above 2's bits if negative or NaN)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool ok = in_range(hi[i]);
-      bad |= !ok;
-      hi[i] = ok ? hi[i] : 0.f;
-      lo[i] = 0.f;
-    }
-    if (k == 0) return;
-    if (!draft) {
-      for (int j = 0; j < k; ++j) {
-        const uint32_t at = (uint32_t)(sh.gone[j] - first);
+  for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(f[i]));
+  if (most <= 0x40000000u) return false;
+  bool bad = false;
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (at == (uint32_t)i) hi[i] = 0.f;
-      }
-      return;
-    }
-    float q[N];
-    Prob<E>::all(vq, q);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool ok = in_range(q[i]);
-      bad |= !ok;
-      const float f = ok ? q[i] : 0.f;
-      const float t = f * b_hi, e = fmaf(f, b_lo, fmaf(f, b_hi, -t));  // f B = t + e
-      const float d = hi[i] - t, v = d - hi[i];
-      const float l = ((hi[i] - (d - v)) - (t + v)) - e;  // hi - t = d + the first difference, exactly
-      const bool some = d + l > 0.f;
-      hi[i] = some ? d : 0.f;
-      lo[i] = some ? l : 0.f;
+    for (int j = 0; j < N; ++j) {
+      if (i == j && !in_range(f[j])) f[j] = 0.f, bad = true;
     }
   }
-};
-
-template <typename T>
-__device__ __forceinline__ T warp_sum(T x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  return x;
+  for (int i = 0; i < N; ++i) f[i] += 0.f;  // (-0 is 0)
+  return bad;
+}
+
+__device__ __forceinline__ void copy16(const void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The walk's state, in CTA 0's first warp (every lane the same).
@@ -208,8 +186,10 @@ struct Walk {
 };
 
 template <typename E, int CS>
-__global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid_constant__ ft_verify_args a) {
-  __shared__ Shared sh;
+__global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(const __grid_constant__ ft_verify_args a) {
+  constexpr int N = Prob<E>::N;
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem);
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -230,49 +210,42 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
     if (rank == 0 && tid == 0) a.n_accepted[b] = 0, a.next_token[b] = -1;
     return;
   }
-  auto node_at = [&](int i, int at) {  // row i; its entries if its parent is `at` (or whatever it is, at < 0)
-    Node x;
-    x.parent = a.parents ? a.parents[q0 + i] : i - 1;
-    x.token = a.tokens[q0 + i];
-    x.u = a.accept_u[q0 + i];
-    x.p = 0.f, x.q = 1.f;
-    const int from = at < 0 ? x.parent : at;
-    if (x.token >= 0 && x.token < a.V && from >= 0 && from < i) {
-      const Row r = row_at<E>(a, q0 + from);
-      x.p = Prob<E>::one(r.p, x.token);
-      if (r.q) x.q = Prob<E>::one(r.q, x.token);
-    }
-    return x;
-  };
+  // (CTA 0 may write into another's shared memory once all have started)
   if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  if (rank == 0) {
-    for (int i = tid; i < min(n, kNodes); i += kThreads)
-      if (i > 0) sh.nodes[i] = node_at(i, -1);
-    __syncthreads();
-  }
-  if constexpr (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
   Walk w{0, 0, 0, 0, true, 1.0, 0.0};
-  bool bad = false, bad_token = false, bad_tree = false;
+  // A lane's row of the window of 32 that is looked at: its parent, token, number and entries.
+  int window = -32, parent = -1, token = -1;
+  float u = 0.f, px = 0.f, qx = 1.f;
+  bool bad = false, bad_token = false, bad_tree = false, started = CS == 1;
   for (;;) {
     if (rank == 0 && warp == 0) {
       int command = kDraw;
       for (;;) {
-        // the next child of w.at
-        int child = -1;
-        for (int i0 = w.last + 1; i0 < n && child < 0; i0 += 32) {
-          const int i = i0 + lane;
-          int parent = -1;
-          if (i < n) parent = i < kNodes ? sh.nodes[i].parent : a.parents ? a.parents[q0 + i] : i - 1;
-          const uint32_t hit = __ballot_sync(~0u, i < n && parent == w.at);
-          if (hit) child = i0 + __ffs(hit) - 1;
+        // the next child of w.at (a child's row comes after its parent's)
+        const uint32_t hit = __ballot_sync(~0u, parent == w.at && window + lane > w.last);
+        if (!hit) {
+          if (window + 32 >= n) break;
+          window += 32;
+          const int i = window + lane;
+          parent = token = -1;
+          if (i < n && i > 0) {
+            parent = a.parents ? a.parents[q0 + i] : i - 1;
+            token = a.tokens[q0 + i];
+            u = below_one(a.accept_u[q0 + i]);
+            px = 0.f, qx = 1.f;
+            if (token >= 0 && token < a.V && parent >= 0 && parent < i) {
+              const Row r = row_at<E>(a, q0 + parent);
+              px = Prob<E>::one(r.p, token);
+              if (r.q) qx = Prob<E>::one(r.q, token);
+            }
+          }
+          continue;
         }
-        if (child < 0) break;
-        Node x;
-        if (child < kNodes)
-          x = sh.nodes[child];
-        else
-          x = node_at(child, w.at);
-        if (x.token < 0 || x.token >= a.V) {
+        const int from = __ffs(hit) - 1, child = window + from;
+        const int x = __shfl_sync(~0u, token, from);
+        const float ux = __shfl_sync(~0u, u, from);
+        float p = __shfl_sync(~0u, px, from), q = __shfl_sync(~0u, qx, from);
+        if (x < 0 || x >= a.V) {
           bad_token = true;
           w.last = child;
           continue;
@@ -286,22 +259,29 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
           command = kSum;
           break;
         }
-        const bool ok_p = in_range(x.p), ok_q = in_range(x.q);
-        bad |= !ok_p || !ok_q;
-        const double p = ok_p ? x.p : 0.f, q = ok_q ? x.q : 0.f, u = below_one(x.u);
-        double left = p;
-        if (a.draft_probs) {
-          left = fmax(p - q * w.B, 0.0);
+        if (!in_range(p)) p = 0.f, bad = true;
+        if (!in_range(q)) q = 0.f, bad = true;
+        bool yes;
+        double left = 0.0;
+        if (w.k == 0) {  // u q < p, exactly: the product is t + e
+          const float t = ux * q, e = fmaf(ux, q, -t);
+          yes = t < p || (t == p && e < 0.f);
         } else {
-          for (int j = 0; j < w.k; ++j)
-            if (sh.gone[j] == x.token) left = 0.0;
+          left = p;
+          if (a.draft_probs) {
+            left = fmax(p - q * w.B, 0.0);
+          } else {
+            for (int j = 0; j < w.k; ++j)
+              if (sh.gone[j] == x) left = 0.0;
+          }
+          yes = (double)ux * q * w.A < left;
         }
         w.last = child;
-        if (u * q * w.A < left) {  // (exact before the first rejection: two fp32 numbers' product)
+        if (yes) {
           if (lane == 0) a.accepted[q0 + w.count] = child;
           w = Walk{child, child, 0, w.count + 1, true, 1.0, 0.0};
         } else {
-          if (lane == 0) sh.gone[w.k] = x.token;
+          if (lane == 0) sh.gone[w.k] = x;
           __syncwarp();
           w.B += w.A;
           // without draft probabilities the next A is known once one sum is
@@ -309,6 +289,9 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
           if (w.known) w.A -= left;
           ++w.k;
         }
+      }
+      if constexpr (CS > 1) {
+        if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       }
       // what the cluster does next: sums of a at (at, k), then the draw
       if (lane < CS) {
@@ -320,57 +303,129 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
         to->b_lo = (float)(w.B - (double)(float)w.B);
         for (int j = 0; j < w.k; ++j) to->gone[j] = sh.gone[j];
       }
+    } else if constexpr (CS > 1) {
+      if (!started) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
+    started = true;
     everyone();
     const int command = sh.command;
+    const float b_hi = sh.b_hi, b_lo = sh.b_lo;
     int k = sh.k;
     const Row r = row_at<E>(a, q0 + sh.row);
-    constexpr int N = Prob<E>::N;
     const int per = (r.groups + CS * kWarps - 1) / (CS * kWarps);
     const int g0 = (rank * kWarps + warp) * per, g1 = min(g0 + per, r.groups);
     const bool vec = r.off >= 0;
     const int base = (vec ? r.off : 0) - N;  // first element of group 0
-    // A stretch is gone through kBatch vectors a lane at a time; a piece is one such step, or several of a long one.
-    const int steps = (per + 32 * kBatch - 1) / (32 * kBatch), to_piece = (steps + kPieces - 1) / kPieces;
-    const float b_hi = sh.b_hi, b_lo = sh.b_lo;
-    uint64_t total = 0;
+    // A lane takes every 32nd vector of its warp's stretch; a piece is some rounds of that.
+    const int rounds = (per + 31) / 32, piece = max(1, (rounds + kPieces * kPiece - 1) / (kPieces * kPiece)) * kPiece;
+    uint64_t left = 0;   // of the point, from the round begun with
+    bool draw = false;
+    int round0 = 0;
     for (;;) {
-      uint64_t sum = 0, piece = 0;
-      float size = 0.f;
-      for (int step = 0; step < steps; ++step) {
-        const int g = g0 + step * 32 * kBatch + lane;
-        uint4 vp[kBatch], vq[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int first = base + (g + 32 * i) * N;
-          vp[i] = vq[i] = make_uint4(0, 0, 0, 0);
-          if (g + 32 * i < g1) {
-            vp[i] = load<E>(r.p, vec, first, a.V);
-            if (r.q && k > 0) vq[i] = load<E>(r.q, vec, first, a.V);
+      auto copy = [&](int round) {
+        const int g = g0 + round * 32 + lane, first = base + g * N;
+        uint4* to = &sh.ring[round % kDepth][0][tid];
+        if (g < g1) {
+          if (vec && first >= 0 && first + N <= a.V) {
+            copy16(to, static_cast<const uint8_t*>(r.p) + (int64_t)first * (16 / N));
+            if (r.q && k > 0) copy16(to + kThreads, static_cast<const uint8_t*>(r.q) + (int64_t)first * (16 / N));
+          } else {
+            *to = load_edge<E>(r.p, first, a.V);
+            if (r.q && k > 0) to[kThreads] = load_edge<E>(r.q, first, a.V);
           }
         }
-        Levels s;
+        copy_commit();
+      };
+#pragma unroll 1
+      for (int i = 0; i < kDepth; ++i) copy(round0 + i);
+      Levels sum;
+      uint32_t count = 0;
+      uint64_t whole_sum = 0, piece_sum = 0;
+      float size = 0.f;
+#pragma unroll 1
+      for (int round = round0; round < rounds; ++round) {
+        copy_wait<kDepth - 1>();
+        const int g = g0 + round * 32 + lane, first = base + g * N;
+        float hi[N], lo[N];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          Weights<E> x;
-          x.make(sh, vp[i], vq[i], r.q != nullptr, base + (g + 32 * i) * N, k, b_hi, b_lo);
-          bad |= x.bad;
+        for (int i = 0; i < N; ++i) hi[i] = lo[i] = 0.f;
+        if (g < g1) {
+          bad |= numbers<E>(sh.ring[round % kDepth][0][tid], hi);
+          if (k > 0) {
+            if (r.q) {
+              float q[N];
+              bad |= numbers<E>(sh.ring[round % kDepth][1][tid], q);
 #pragma unroll
-          for (int j = 0; j < N; ++j) s.add(x.hi[j], x.lo[j]);
+              for (int i = 0; i < N; ++i) {
+                const float t = q[i] * b_hi, e = fmaf(q[i], b_lo, fmaf(q[i], b_hi, -t));  // q B = t + e
+                const float d = hi[i] - t, l = ((hi[i] - d) - t) - e;                     // exact where p >= t / 2
+                const bool some = d + l > 0.f;
+                hi[i] = some ? d : 0.f;
+                lo[i] = some ? l : 0.f;
+              }
+            } else {
+              for (int j = 0; j < k; ++j) {
+                const uint32_t at = (uint32_t)(sh.gone[j] - first);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                  if (at == (uint32_t)i) hi[i] = 0.f;
+              }
+            }
+          }
         }
-        s.finish(kBatch * N);
-        // (the first level's number in two parts: a warp's could pass 32 bits)
-        const uint32_t up = __reduce_add_sync(~0u, s.a >> 12), low = __reduce_add_sync(~0u, s.a & 0xFFFu);
-        const int32_t b32 = __reduce_add_sync(~0u, (int32_t)s.b), c32 = __reduce_add_sync(~0u, (int32_t)s.c);
-        piece += (((uint64_t)up << 12) + low << (kUnit - 22)) + ((int64_t)b32 << (kUnit - 40)) + (int64_t)c32;
-        size += (float)up * 0x1p-10f;
-        if (step + 1 == steps || (step + 1) % to_piece == 0) {
-          if (lane == 0) sh.piece[warp][step / to_piece] = piece;
-          sum += piece;
-          piece = 0;
+        copy(round + kDepth);
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum.add(hi[i], lo[i]);
+        count += N;
+        if (draw) {
+          sum.finish(count);
+          const uint64_t mine = sum.value();
+          uint64_t upto = mine;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const uint32_t hit = __ballot_sync(~0u, upto > left);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) {
+              uint64_t c = upto - mine;
+              int next = -1;
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                Levels one;
+                one.add(hi[i], lo[i]);
+                one.finish(1);
+                c += one.value();
+                if (next < 0 && c > left) next = first + i;
+              }
+              a.next_token[b] = next;
+            }
+            break;
+          }
+          left -= __shfl_sync(~0u, upto, 31);
+          sum = Levels();
+          count = 0;
+        } else if ((round + 1) % kPiece == 0 || round + 1 == rounds) {
+          sum.finish(count);
+          // (the first level's number in two parts: a warp's could pass 32 bits)
+          const uint32_t up = __reduce_add_sync(~0u, sum.a >> 12), low = __reduce_add_sync(~0u, sum.a & 0xFFFu);
+          const int32_t sb = __reduce_add_sync(~0u, (int32_t)sum.b), sc = __reduce_add_sync(~0u, (int32_t)sum.c);
+          const uint64_t value = ((((uint64_t)up << 12) + low) << (kUnit - 22)) + ((int64_t)sb << (kUnit - 40)) + (int64_t)sc;
+          whole_sum += value;
+          piece_sum += value;
+          if ((round + 1) % piece == 0 || round + 1 == rounds) {
+            if (lane == 0) sh.piece[warp][round / piece] = piece_sum;
+            piece_sum = 0;
+          }
+          size += (float)up * 0x1p-10f;
+          sum = Levels();
+          count = 0;
         }
       }
-      if (lane == 0) sh.warp_sum[warp] = sum, sh.warp_size[warp] = size;
+      copy_wait<0>();
+      if (draw) break;
+      if (lane == 0) sh.warp_sum[warp] = whole_sum, sh.warp_size[warp] = size;
       __syncthreads();
       if (tid < CS) {
         uint64_t s = 0;
@@ -381,108 +436,56 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
         to->cta_size[rank] = z;
       }
       everyone();
+      uint64_t total = 0, before = 0;
       float whole = 0.f;
-      total = 0;
-      for (int i = 0; i < CS; ++i) total += sh.cta_sum[i], whole += sh.cta_size[i];
+#pragma unroll 1
+      for (int i = 0; i < CS; ++i) {
+        if (i == rank) before = total;
+        total += sh.cta_sum[i];
+        whole += sh.cta_size[i];
+      }
       if (whole > 8.f) {
         total = 0;
         bad = true;
       }
-      if (command == kSum || total > 0 || k == 0) break;
-      k = 0;  // nothing is left of a: the draw is from p
-      everyone();
-    }
-    if (command == kSum) {
-      if (rank == 0 && warp == 0) {
+      if (command == kSum) {
         w.A = (double)total * 0x1p-59;
         w.known = true;
+        break;
       }
-      everyone();  // (the sums have been read)
-      continue;
-    }
-    // the draw
-    if (total == 0) {
-      bad = true;
-      if (rank == 0 && tid == 0) a.next_token[b] = -1;
-    } else {
+      if (total == 0 && k > 0) {  // nothing is left of a: the draw is from p
+        k = 0;
+        everyone();
+        continue;
+      }
+      if (total == 0) {
+        bad = true;
+        if (rank == 0 && tid == 0) a.next_token[b] = -1;
+        break;
+      }
       // floor(u total): a whole running sum is above u total where it is above that
       const uint32_t bits = __float_as_uint(below_one(a.draw_u[b]));
       const int shift = 150 - max((int)(bits >> 23), 1);
       const uint32_t m = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
       const uint64_t point = shift >= 128 ? 0 : (uint64_t)(((unsigned __int128)total * m) >> shift);
-      uint64_t before = 0;
-      for (int i = 0; i < rank; ++i) before += sh.cta_sum[i];
-      if (point >= before && point - before < sh.cta_sum[rank]) {
-        uint64_t left = point - before;
-        for (int i = 0; i < warp; ++i) {
-          if (left < sh.warp_sum[i]) {
-            left = ~0ull;
-            break;
-          }
-          left -= sh.warp_sum[i];
-        }
-        if (left != ~0ull && left < sh.warp_sum[warp]) {  // this warp's stretch holds the point
-          int step = 0;
-          for (int at = 0; left >= sh.piece[warp][at]; ++at) {  // (their sum is above it)
-            left -= sh.piece[warp][at];
-            step += to_piece;
-          }
-          bool found = false;
-          for (; step < steps && !found; ++step) {
-            const int gg = g0 + step * 32 * kBatch + lane;
-            uint4 vp[kBatch], vq[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int first = base + (gg + 32 * i) * N;
-              vp[i] = vq[i] = make_uint4(0, 0, 0, 0);
-              if (gg + 32 * i < g1) {
-                vp[i] = load<E>(r.p, vec, first, a.V);
-                if (r.q && k > 0) vq[i] = load<E>(r.q, vec, first, a.V);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              if (found) break;
-              const int first = base + (gg + 32 * i) * N;
-              Weights<E> x;
-              x.make(sh, vp[i], vq[i], r.q != nullptr, first, k, b_hi, b_lo);
-              auto value = [&](int j) {
-                Levels s;
-                s.add(x.hi[j], x.lo[j]);
-                s.finish(1);
-                return s.value();
-              };
-              uint64_t mine = 0;
-#pragma unroll
-              for (int j = 0; j < N; ++j) mine += value(j);
-              uint64_t upto = mine;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t y = __shfl_up_sync(~0u, upto, o);
-                if (lane >= o) upto += y;
-              }
-              const uint32_t hit = __ballot_sync(~0u, upto > left);
-              if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                  uint64_t c = upto - mine;
-                  int token = -1;
-#pragma unroll
-                  for (int j = 0; j < N; ++j) {
-                    c += value(j);
-                    if (token < 0 && c > left) token = first + j;
-                  }
-                  a.next_token[b] = token;
-                }
-                found = true;
-              } else {
-                left -= __shfl_sync(~0u, upto, 31);
-              }
-            }
-          }
-        }
+      if (point < before || point - before >= sh.cta_sum[rank]) break;
+      left = point - before;
+      bool mine = true;
+#pragma unroll 1
+      for (int i = 0; i < warp && mine; ++i) {
+        mine = left >= sh.warp_sum[i];
+        left -= sh.warp_sum[i];
       }
+      if (!mine || left >= sh.warp_sum[warp]) break;
+      // this warp's stretch holds the point
+      for (int i = 0; left >= sh.piece[warp][i]; ++i) {  // (their sum is above it)
+        left -= sh.piece[warp][i];
+        round0 += piece;
+      }
+      draw = true;
     }
-    break;
+    if (command == kDraw) break;
+    everyone();  // (the sums have been read)
   }
   if (rank == 0 && warp == 0) {
     if (lane == 0) a.n_accepted[b] = w.count;
@@ -492,14 +495,23 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const __grid
     const uint32_t said = (bad ? FT_ST_NAN : 0u) | (bad_token ? FT_ST_BAD_TOKEN : 0u) | (bad_tree ? FT_ST_BAD_TREE : 0u);
     if (said) atomicOr(a.status, said);
   }
-  everyone();  // no CTA leaves while another may still write into its shared memory
 }
 
 template <typename E, int CS>
 cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
+  static thread_local int configured = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured != dev) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    configured = dev;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)a.num_reqs * CS);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -514,8 +526,11 @@ cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_cs(const ft_verify_args& a, cudaStream_t st) {
+  // As many CTAs a request as are resident together, while a lane has more than one piece of a row.
   int cs = 1;
-  while (cs < kMaxCluster && (int64_t)a.num_reqs * cs < 4 * sm_count() && a.V / Prob<E>::N / cs > kThreads * kBatch) cs *= 2;
+  while (cs < kMaxCluster && (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident &&
+         a.V / Prob<E>::N / cs > kThreads * kPiece)
+    cs *= 2;
   switch (cs) {
     case 1: return launch<E, 1>(a, st);
     case 2: return launch<E, 2>(a, st);

@@ -12,21 +12,23 @@
 // The token is a whole number next to borders of the running sum: fp32 sums over
 // 131072 entries would move the borders by more than many entries are wide, and
 // 64-bit floating point runs at a sixty-fourth of the rate.  So entries are cut into
-// whole numbers at three levels (multiples of 2^-22, 2^-40 and 2^-59; adding a
-// constant leaves each level's number in the sum's low bits) and added as such:
-// sums do not depend on their order.  After k rejections
+// whole numbers at two levels (multiples of 2^-22 and 2^-45; adding a constant
+// leaves each level's number in the sum's low bits) and added as such: sums do not
+// depend on their order.  After k rejections
 //   a = max(p - q B, 0),  B = 1 + A_1 + .. + A_(k-1)
 // (what one step cuts off at 0 the next ones would take below it), so a is never
-// stored and takes one product, in two fp32 numbers: exact to 2^-46.
+// stored and takes one product, in two fp32 numbers (to 2^-46).
 //
 // A cluster of CTAs shares a request.  CTA 0 walks, a row of the request a lane,
 // and says what the cluster does next; every warp sums one stretch of the row and
 // keeps its pieces' sums, and the piece that holds the drawn point is gone through
-// once more, by the same loop.  Vectors come through shared memory (a thread's own,
-// kDepth ahead), so that the loop stays rolled: one request is bound by latency, and
-// with four vectors' arithmetic unrolled twice most of it was the instructions'
-// (15000 cycles for a row's eighth, first time through).
+// once more.  Vectors come through shared memory (a thread's own, kDepth rounds
+// ahead).  One request is bound by latency, so the loop over them has no branches
+// but for unusual numbers (with them a round of 8 numbers took 2400 cycles) and its
+// code is short.
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "attn_side.h"
 #include "tma.h"
@@ -37,13 +39,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kRejected = 64;
-constexpr int kUnit = 59;  // sums are in units of 2^-59
-constexpr int kDepth = 8;     // vectors of a thread on their way
-constexpr int kPieces = 64;   // of a warp's stretch at most
-constexpr int kPiece = 4;     // vectors a lane of a piece, or a multiple
-constexpr int kResident = 2;  // CTAs of an SM
+constexpr int kUnit = 45;  // sums are in units of 2^-45
+constexpr int kNumbers = 8;  // of a thread in a round
+constexpr int kDepth = 3;    // rounds on their way
+constexpr int kResident = 4;  // CTAs of an SM
+constexpr int kPieces = 64;  // of a warp's stretch at most: a round each, or several
 
 template <typename E>
 struct Prob {  // a 16-byte vector of a row
@@ -73,33 +75,31 @@ __device__ __forceinline__ bool in_range(float v) { return v >= 0.f && v <= 2.f;
 // A random number as it is used.
 __device__ __forceinline__ float below_one(float u) { return u > 0.f ? fminf(u, 0.99999994f) : 0.f; }
 
-// Sums of numbers hi + lo in [0, 2] (|lo| <= 2^-24 hi) as whole numbers at three
-// levels; each counts the constants' bits once a number.
+// Sums of pairs of numbers hi + lo in [0, 2] (|lo| <= 2^-24 hi) as whole numbers at
+// two levels; each counts the constants' bits once a number.
 struct Levels {
-  uint32_t a = 0, b = 0, c = 0;
-  static constexpr float kA = 2.f, kB = 0x1.8p-17f, kC = 0x1.8p-36f;
-  __device__ __forceinline__ void add(float hi, float lo) {
-    const float s = hi + kA, r = (hi - (s - kA)) + lo;
-    const float t = r + kB, q = r - (t - kB);
-    a += __float_as_uint(s);
-    b += __float_as_uint(t);
-    c += __float_as_uint(q + kC);
+  uint32_t a = 0, b = 0;
+  static constexpr float kA = 2.f, kB = 0x1.8p-22f;
+  __device__ __forceinline__ void add(uint64_t hi, uint64_t lo) {
+    const uint64_t minus = pair2(-1.f, -1.f);
+    const uint64_t s = add2(hi, pair2(kA, kA));
+    const uint64_t r = add2(fma2(add2(s, pair2(-kA, -kA)), minus, hi), lo);
+    const float2 x = split2(s), y = split2(add2(r, pair2(kB, kB)));
+    a += __float_as_uint(x.x) + __float_as_uint(x.y);
+    b += __float_as_uint(y.x) + __float_as_uint(y.y);
   }
   // What `n` numbers gave, without the constants.
   __device__ __forceinline__ void finish(uint32_t n) {
     a -= n * __float_as_uint(kA);
     b -= n * __float_as_uint(kB);
-    c -= n * __float_as_uint(kC);
   }
-  __device__ __forceinline__ uint64_t value() const {
-    return ((uint64_t)a << (kUnit - 22)) + ((int64_t)(int32_t)b << (kUnit - 40)) + (int64_t)(int32_t)c;
-  }
+  __device__ __forceinline__ uint64_t value() const { return ((uint64_t)a << (kUnit - 22)) + (int64_t)(int32_t)b; }
 };
 
 enum Command : int { kSum, kDraw };
 
 struct Shared {
-  uint4 ring[kDepth][2][kThreads];
+  uint4 ring[kDepth][2][kNumbers / 4][kThreads];
   // what CTA 0 says
   int command, row, k;  // the row that is read (in the batch), rejections so far
   float b_hi, b_lo;     // B
@@ -147,26 +147,10 @@ __device__ __noinline__ uint4 load_edge(const void* row, int first, int V) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A vector's numbers; those outside [0, 2] become 0, and whether there are any.
-template <typename E>
-__device__ __forceinline__ bool numbers(const uint4& v, float* f) {
-  constexpr int N = Prob<E>::N;
-  Prob<E>::all(v, f);
-  uint32_t most = 0;  // (as whole numbers: above 2's bits if negative or NaN)
-#pragma unroll
-  for (int i = 0; i < N; ++i) most = max(most, __float_as_uint(f[i]));
-  if (most <= 0x40000000u) return false;
-  bool bad = false;
-#pragma unroll 1
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (i == j && !in_range(f[j])) f[j] = 0.f, bad = true;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) f[i] += 0.f;  // (-0 is 0)
-  return bad;
+// Numbers outside [0, 2] become 0.
+template <int COUNT>
+__device__ __noinline__ void mend(float* f) {
+  for (int i = 0; i < COUNT; ++i) f[i] = in_range(f[i]) ? f[i] + 0.f : 0.f;  // (-0 is 0)
 }
 
 __device__ __forceinline__ void copy16(const void* dst, const void* src) {
@@ -316,115 +300,138 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
     const int g0 = (rank * kWarps + warp) * per, g1 = min(g0 + per, r.groups);
     const bool vec = r.off >= 0;
     const int base = (vec ? r.off : 0) - N;  // first element of group 0
-    // A lane takes every 32nd vector of its warp's stretch; a piece is some rounds of that.
-    const int rounds = (per + 31) / 32, piece = max(1, (rounds + kPieces * kPiece - 1) / (kPieces * kPiece)) * kPiece;
-    uint64_t left = 0;   // of the point, from the round begun with
-    bool draw = false;
-    int round0 = 0;
-    for (;;) {
-      auto copy = [&](int round) {
-        const int g = g0 + round * 32 + lane, first = base + g * N;
-        uint4* to = &sh.ring[round % kDepth][0][tid];
-        if (g < g1) {
-          if (vec && first >= 0 && first + N <= a.V) {
-            copy16(to, static_cast<const uint8_t*>(r.p) + (int64_t)first * (16 / N));
-            if (r.q && k > 0) copy16(to + kThreads, static_cast<const uint8_t*>(r.q) + (int64_t)first * (16 / N));
-          } else {
-            *to = load_edge<E>(r.p, first, a.V);
-            if (r.q && k > 0) to[kThreads] = load_edge<E>(r.q, first, a.V);
-          }
+    // A lane takes every 32nd vector of its warp's stretch, kVecs of them a round.
+    constexpr int kVecs = kNumbers / N;
+    const int rounds = (per + 32 * kVecs - 1) / (32 * kVecs), piece = (rounds + kPieces - 1) / kPieces;
+    const int limit = base + g1 * N;  // of the stretch
+    auto first_of = [&](int round, int v) { return base + (g0 + (round * kVecs + v) * 32 + lane) * N; };
+    auto copy = [&](int round) {
+      if (round >= rounds) return copy_commit();
+      const int first = first_of(round, 0);
+      uint4* to = &sh.ring[round % kDepth][0][0][tid];
+      const bool q = r.q && k > 0;
+      const int last = first - lane * N + (kVecs * 32 - 1) * N;  // the round's last vector
+      if (vec && first >= lane * N && last + N <= a.V && last < limit) {
+        const uint8_t* from = static_cast<const uint8_t*>(r.p) + (int64_t)first * (16 / N);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) copy16(to + v * kThreads, from + v * 512);
+        if (q) {
+          from = static_cast<const uint8_t*>(r.q) + (int64_t)first * (16 / N);
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) copy16(to + (kNumbers / 4 + v) * kThreads, from + v * 512);
         }
-        copy_commit();
-      };
+      } else {
 #pragma unroll 1
-      for (int i = 0; i < kDepth; ++i) copy(round0 + i);
-      Levels sum;
-      uint32_t count = 0;
-      uint64_t whole_sum = 0, piece_sum = 0;
-      float size = 0.f;
+        for (int v = 0; v < kVecs; ++v) {
+          const int at = first + v * 32 * N;
+          const bool inside = vec && at >= 0 && at + N <= a.V, some = at < limit;
 #pragma unroll 1
-      for (int round = round0; round < rounds; ++round) {
-        copy_wait<kDepth - 1>();
-        const int g = g0 + round * 32 + lane, first = base + g * N;
-        float hi[N], lo[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) hi[i] = lo[i] = 0.f;
-        if (g < g1) {
-          bad |= numbers<E>(sh.ring[round % kDepth][0][tid], hi);
-          if (k > 0) {
-            if (r.q) {
-              float q[N];
-              bad |= numbers<E>(sh.ring[round % kDepth][1][tid], q);
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const float t = q[i] * b_hi, e = fmaf(q[i], b_lo, fmaf(q[i], b_hi, -t));  // q B = t + e
-                const float d = hi[i] - t, l = ((hi[i] - d) - t) - e;                     // exact where p >= t / 2
-                const bool some = d + l > 0.f;
-                hi[i] = some ? d : 0.f;
-                lo[i] = some ? l : 0.f;
-              }
-            } else {
-              for (int j = 0; j < k; ++j) {
-                const uint32_t at = (uint32_t)(sh.gone[j] - first);
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                  if (at == (uint32_t)i) hi[i] = 0.f;
-              }
-            }
+          for (int z = 0; z < (q ? 2 : 1); ++z) {
+            uint4* slot = to + (z * (kNumbers / 4) + v) * kThreads;
+            const void* row = z ? r.q : r.p;
+            if (some && inside)
+              copy16(slot, static_cast<const uint8_t*>(row) + (int64_t)at * (16 / N));
+            else
+              *slot = some ? load_edge<E>(row, at, a.V) : make_uint4(0, 0, 0, 0);
           }
-        }
-        copy(round + kDepth);
-#pragma unroll
-        for (int i = 0; i < N; ++i) sum.add(hi[i], lo[i]);
-        count += N;
-        if (draw) {
-          sum.finish(count);
-          const uint64_t mine = sum.value();
-          uint64_t upto = mine;
-#pragma unroll 1
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(~0u, upto, o);
-            if (lane >= o) upto += y;
-          }
-          const uint32_t hit = __ballot_sync(~0u, upto > left);
-          if (hit) {
-            if (lane == __ffs(hit) - 1) {
-              uint64_t c = upto - mine;
-              int next = -1;
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                Levels one;
-                one.add(hi[i], lo[i]);
-                one.finish(1);
-                c += one.value();
-                if (next < 0 && c > left) next = first + i;
-              }
-              a.next_token[b] = next;
-            }
-            break;
-          }
-          left -= __shfl_sync(~0u, upto, 31);
-          sum = Levels();
-          count = 0;
-        } else if ((round + 1) % kPiece == 0 || round + 1 == rounds) {
-          sum.finish(count);
-          // (the first level's number in two parts: a warp's could pass 32 bits)
-          const uint32_t up = __reduce_add_sync(~0u, sum.a >> 12), low = __reduce_add_sync(~0u, sum.a & 0xFFFu);
-          const int32_t sb = __reduce_add_sync(~0u, (int32_t)sum.b), sc = __reduce_add_sync(~0u, (int32_t)sum.c);
-          const uint64_t value = ((((uint64_t)up << 12) + low) << (kUnit - 22)) + ((int64_t)sb << (kUnit - 40)) + (int64_t)sc;
-          whole_sum += value;
-          piece_sum += value;
-          if ((round + 1) % piece == 0 || round + 1 == rounds) {
-            if (lane == 0) sh.piece[warp][round / piece] = piece_sum;
-            piece_sum = 0;
-          }
-          size += (float)up * 0x1p-10f;
-          sum = Levels();
-          count = 0;
         }
       }
+      copy_commit();
+    };
+    // A round's numbers from slot z of the ring; where one is outside [0, 2], mended and reported.
+    auto numbers = [&](int round, int z, float* f) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) Prob<E>::all(sh.ring[round % kDepth][z][v][tid], f + v * N);
+      uint32_t most = 0;  // (as whole numbers: above 2's bits if negative or NaN)
+#pragma unroll
+      for (int i = 0; i < kNumbers; ++i) most = max(most, __float_as_uint(f[i]));
+      if (most > 0x40000000u) {
+        float t[kNumbers];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < kNumbers; ++i) t[i] = f[i], odd |= !in_range(f[i]);
+        mend<kNumbers>(t);
+        bad |= odd;
+#pragma unroll
+        for (int i = 0; i < kNumbers; ++i) f[i] = t[i];
+      }
+    };
+    // What is left of a round's numbers, as hi + lo: pairs of neighbours.  `how`: nothing rejected, drafts without or
+    // with probabilities.
+    auto weights = [&](auto how, int round, uint64_t* hi, uint64_t* lo) {
+      float p[kNumbers];
+      numbers(round, 0, p);
+      if constexpr (how == 1) {
+        for (int j = 0; j < k; ++j) {
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) {
+            const uint32_t at = (uint32_t)(sh.gone[j] - first_of(round, v));
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (at == (uint32_t)i) p[v * N + i] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kNumbers / 2; ++i) hi[i] = pair2(p[2 * i], p[2 * i + 1]), lo[i] = 0;
+      if constexpr (how == 2) {
+        float q[kNumbers];
+        numbers(round, 1, q);
+        const uint64_t bh = pair2(b_hi, b_hi), bl = pair2(b_lo, b_lo), mh = pair2(-b_hi, -b_hi), minus = pair2(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < kNumbers / 2; ++i) {
+          const uint64_t f = pair2(q[2 * i], q[2 * i + 1]), t = mul2(f, mh);  // q B = -t + e
+          const uint64_t e = fma2(f, bl, fma2(f, bh, t));
+          const uint64_t d = add2(hi[i], t);
+          const uint64_t l = fma2(e, minus, add2(fma2(d, minus, hi[i]), t));  // d + l = p - q B, exactly where p >= q B / 2
+          const float2 x = split2(d), y = split2(l), z = split2(add2(d, l));
+          hi[i] = pair2(z.x > 0.f ? x.x : 0.f, z.y > 0.f ? x.y : 0.f);
+          lo[i] = pair2(z.x > 0.f ? y.x : 0.f, z.y > 0.f ? y.y : 0.f);
+        }
+      }
+    };
+    const std::integral_constant<int, 0> plain;
+    const std::integral_constant<int, 1> without;
+    const std::integral_constant<int, 2> with;
+    for (;;) {
+      uint64_t whole_sum = 0;
+      float size = 0.f;
+      auto pass = [&](auto how) {
+        uint64_t piece_sum = 0;
+        int left = piece, at = 0;
+#pragma unroll 1
+        for (int i = 0; i < kDepth; ++i) copy(i);
+#pragma unroll 1
+        for (int round = 0; round < rounds; ++round) {
+          copy_wait<kDepth - 1>();
+          Levels sum;
+          uint64_t hi[kNumbers / 2], lo[kNumbers / 2];
+          weights(how, round, hi, lo);
+#pragma unroll
+          for (int i = 0; i < kNumbers / 2; ++i) sum.add(hi[i], lo[i]);
+          copy(round + kDepth);
+          sum.finish(kNumbers);
+          // (the first level's number in two parts: a warp's could pass 32 bits)
+          const uint32_t up = __reduce_add_sync(~0u, sum.a >> 12), low = __reduce_add_sync(~0u, sum.a & 0xFFFu);
+          const int32_t rest = __reduce_add_sync(~0u, (int32_t)sum.b);
+          piece_sum += ((((uint64_t)up << 12) + low) << (kUnit - 22)) + (int64_t)rest;
+          size += (float)up * 0x1p-10f;
+          if (--left == 0 || round + 1 == rounds) {
+            if (lane == 0) sh.piece[warp][at] = piece_sum;
+            whole_sum += piece_sum;
+            piece_sum = 0;
+            left = piece;
+            ++at;
+          }
+        }
+      };
+      if (k == 0)
+        pass(plain);
+      else if (!r.q)
+        pass(without);
+      else
+        pass(with);
       copy_wait<0>();
-      if (draw) break;
       if (lane == 0) sh.warp_sum[warp] = whole_sum, sh.warp_size[warp] = size;
       __syncthreads();
       if (tid < CS) {
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
         bad = true;
       }
       if (command == kSum) {
-        w.A = (double)total * 0x1p-59;
+        w.A = (double)total * 0x1p-45;
         w.known = true;
         break;
       }
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
       const uint32_t m = (bits & 0x7FFFFFu) | (bits >> 23 ? 0x800000u : 0u);
       const uint64_t point = shift >= 128 ? 0 : (uint64_t)(((unsigned __int128)total * m) >> shift);
       if (point < before || point - before >= sh.cta_sum[rank]) break;
-      left = point - before;
+      uint64_t left = point - before;
       bool mine = true;
 #pragma unroll 1
       for (int i = 0; i < warp && mine; ++i) {
@@ -478,11 +485,57 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
       }
       if (!mine || left >= sh.warp_sum[warp]) break;
       // this warp's stretch holds the point
+      int round = 0;
       for (int i = 0; left >= sh.piece[warp][i]; ++i) {  // (their sum is above it)
         left -= sh.piece[warp][i];
-        round0 += piece;
+        round += piece;
       }
-      draw = true;
+      bool found = false;
+#pragma unroll 1
+      for (; !found && round < rounds; ++round) {
+        copy(round);
+        copy_wait<0>();
+        uint64_t hi[kNumbers / 2], lo[kNumbers / 2];
+        if (k == 0)
+          weights(plain, round, hi, lo);
+        else if (!r.q)
+          weights(without, round, hi, lo);
+        else
+          weights(with, round, hi, lo);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+          if (found) break;
+          Levels sum;
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) sum.add(hi[v * (N / 2) + i], lo[v * (N / 2) + i]);
+          sum.finish(N);
+          const uint64_t own = sum.value();
+          uint64_t upto = own;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const uint32_t hit = __ballot_sync(~0u, upto > left);
+          if (hit && lane == __ffs(hit) - 1) {
+            uint64_t c = upto - own;
+            int next = -1;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const float2 x = split2(hi[(v * N + i) / 2]), y = split2(lo[(v * N + i) / 2]);
+              Levels one;
+              one.add(pair2(i & 1 ? x.y : x.x, 0.f), pair2(i & 1 ? y.y : y.x, 0.f));
+              one.finish(2);
+              c += one.value();
+              if (next < 0 && c > left) next = first_of(round, v) + i;
+            }
+            a.next_token[b] = next;
+          }
+          found = hit != 0;
+          left -= __shfl_sync(~0u, upto, 31);
+        }
+      }
+      break;
     }
     if (command == kDraw) break;
     everyone();  // (the sums have been read)
@@ -506,6 +559,10 @@ cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
     if (e != cudaSuccess) return e;
+    if (CS > 8) {
+      const cudaError_t e2 = cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e2 != cudaSuccess) return e2;
+    }
     configured = dev;
   }
   cudaLaunchConfig_t cfg{};
@@ -526,16 +583,18 @@ cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_cs(const ft_verify_args& a, cudaStream_t st) {
-  // As many CTAs a request as are resident together, while a lane has more than one piece of a row.
+  // As many CTAs a request as run at once, while a lane has more than one vector of a row.  (A cluster lies in one GPC:
+  // of 16 CTAs they leave a sixth of the places empty and more.  37 requests of 50021 16-bit entries 23 us with 16, 18 with 8.)
   int cs = 1;
-  while (cs < kMaxCluster && (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident &&
-         a.V / Prob<E>::N / cs > kThreads * kPiece)
+  while (cs < kMaxCluster && (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * (cs < 8 ? kResident : 2) &&
+         a.V / Prob<E>::N / cs > kThreads)
     cs *= 2;
   switch (cs) {
     case 1: return launch<E, 1>(a, st);
     case 2: return launch<E, 2>(a, st);
     case 4: return launch<E, 4>(a, st);
-    default: return launch<E, 8>(a, st);
+    case 8: return launch<E, 8>(a, st);
+    default: return launch<E, 16>(a, st);
   }
 }
 

@@ -1,8 +1,9 @@
 """Verification of drafted tokens against a plain 64-bit implementation.
 
-Results are whole numbers and equal: the library's sums are exact to 2^-59 an
-entry, the reference's to about 1e-14, and no random number here lies that near
-a border (but in the test that puts them there with exact sums).
+Results are whole numbers and equal: the library's entries are rounded to
+multiples of 2^-45, sums over a row are off by 2^-46 sqrt(V) or so, and no random
+number here lies that near a border (but in the test that puts them there with
+exact sums).
 """
 import numpy as np
 import pytest

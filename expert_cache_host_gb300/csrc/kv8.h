@@ -19,10 +19,22 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
   asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(v));
   return r;
 }
-// Two floats rounded to e4m3 (nearest even; past 448 in size 448, NaN 0x7F), `lo` in the low byte.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+// Four floats rounded to e4m3 (nearest even; past 448 in size 448, NaN 0x7F), the first in the lowest byte.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   uint32_t r;
-  asm("{ .reg .b16 h; cvt.rn.satfinite.e4m3x2.f32 h, %1, %2; cvt.u32.u16 %0, h; }" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{ .reg .b16 l, h; cvt.rn.satfinite.e4m3x2.f32 l, %2, %1; cvt.rn.satfinite.e4m3x2.f32 h, %4, %3; mov.b32 %0, {l, h}; }"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+// The larger magnitudes of two pairs (signs are of no account; NaN where there is one).
+template <typename E>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (Elem<E>::kDtype == FT_DTYPE_BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 

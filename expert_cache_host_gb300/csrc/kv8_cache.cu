@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSteps = 8;  // 16-byte stretches a lane holds
+constexpr int kSpan = 4;   // requests a lane looks at together
 
 struct StoreArgs {
   ft_kv8_store_args a;
@@ -46,55 +47,62 @@ template <typename E>
 constexpr int kCapByte = Elem<E>::kDtype == FT_DTYPE_BF16 ? 247 : 135;
 
 template <typename E, int D, int W>
-__global__ void __launch_bounds__(kThreads) kv8_store_kernel(const __grid_constant__ StoreArgs g) {
+__global__ void __launch_bounds__(kThreads, 4) kv8_store_kernel(const __grid_constant__ StoreArgs g) {
   constexpr int LPR = D / 8, RPS = 32 / LPR;  // lanes of a row, rows of a warp's step
   const ft_kv8_store_args& a = g.a;
-  __shared__ Rows s_rows;
-  __shared__ int s_b, s_j;
-  __shared__ long long s_sum[kWarps];
   __shared__ uint32_t s_max[kWarps];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The request and block of unit blockIdx.x, from inclusive sums of the requests' blocks.
-  if (tid == 0) s_b = -1;
+  // The request and block of unit blockIdx.x, from sums of the requests' blocks: every warp for itself, 32 * kSpan
+  // requests at a time, their lengths loaded together.
   const int bs_mask = (1 << g.log2_block) - 1;
-  long long base = 0;
-  for (int b0 = 0; b0 < a.num_reqs && base <= (long long)blockIdx.x; b0 += kThreads) {
-    Rows r{};
-    long long cnt = 0;
-    if (b0 + tid < a.num_reqs) {
-      r = rows_of(a, b0 + tid);
-      if (r.n > 0) cnt = (((long long)r.ctx + r.n + bs_mask) >> g.log2_block) - (r.ctx >> g.log2_block);
+  Rows r{};
+  int b = -1, j = 0;
+  for (long long base = 0, b0 = 0; b0 < a.num_reqs; b0 += 32 * kSpan) {
+    Rows mine[kSpan];
+    long long cnt[kSpan], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+      mine[i] = Rows{};
+      if (b0 + lane * kSpan + i < a.num_reqs) mine[i] = rows_of(a, (int)b0 + lane * kSpan + i);
     }
-    long long x = cnt;
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+      cnt[i] = mine[i].n > 0 ? (((long long)mine[i].ctx + mine[i].n + bs_mask) >> g.log2_block) - (mine[i].ctx >> g.log2_block) : 0;
+      sum += cnt[i];
+    }
+    long long x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(~0u, x, o);
       if (lane >= o) x += y;
     }
-    __syncthreads();
-    if (lane == 31) s_sum[warp] = x;
-    __syncthreads();
-    long long all = 0;
+    const uint32_t hit = __ballot_sync(~0u, base + x > (long long)blockIdx.x);
+    if (hit) {
+      const int from = __ffs(hit) - 1;
+      long long at = (long long)blockIdx.x - (base + x - sum);  // the unit's place in the lane's requests
+      int which = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) x += s_sum[w];
-      all += s_sum[w];
+      for (int i = 0; i + 1 < kSpan; ++i) {
+        const bool past = which == i && at >= cnt[i];
+        at -= past ? cnt[i] : 0;
+        which += past ? 1 : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i)
+        if (which == i) r = mine[i];
+      r.q0 = __shfl_sync(~0u, r.q0, from);
+      r.n = __shfl_sync(~0u, r.n, from);
+      r.ctx = __shfl_sync(~0u, r.ctx, from);
+      j = (int)__shfl_sync(~0u, at, from);
+      b = (int)b0 + from * kSpan + __shfl_sync(~0u, which, from);
+      break;
     }
-    x += base;
-    if ((long long)blockIdx.x >= x - cnt && (long long)blockIdx.x < x) {
-      s_rows = r;
-      s_b = b0 + tid;
-      s_j = (int)((long long)blockIdx.x - (x - cnt));
-    }
-    base += all;
+    base += __shfl_sync(~0u, x, 31);
   }
-  __syncthreads();
-  const int b = s_b;
-  if (b < 0) return;
-  const Rows r = s_rows;
-  const long long block0 = ((long long)(r.ctx >> g.log2_block) + s_j) << g.log2_block;  // the block's first token
+  if (b < 0) return;  // (the whole block)
+  const long long block0 = ((long long)(r.ctx >> g.log2_block) + j) << g.log2_block;  // the block's first token
   const int lo = (int)max((long long)r.ctx - block0, 0ll);                              // its new rows are [lo, hi)
   const int hi = (int)min((long long)r.ctx + r.n - block0, (long long)bs_mask + 1);
   const int sub = blockIdx.y * (kWarps / W) + warp / W;
@@ -131,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const __grid_consta
   uint32_t m2 = 0;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i)
-    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                               __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+    m2 = max_abs2<E>(max_abs2<E>(max_abs2<E>(m2, x[i].x), x[i].y), max_abs2<E>(x[i].z, x[i].w));
+  m2 &= 0x7FFF7FFFu;
   uint32_t m = __reduce_max_sync(~0u, max(m2 & 0xFFFFu, m2 >> 16));
   const bool odd = m >= inf;  // infinities or NaN among the warp's numbers
   if (odd) {
@@ -179,32 +187,33 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const __grid_consta
       for (int k = 0; k < 2; ++k) {
         const float2 u = Elem<__half>::unpack(e4m3x2_to_f16x2(w[k] & 0xFFFFu));
         const float2 v = Elem<__half>::unpack(e4m3x2_to_f16x2(w[k] >> 16));
-        o[k] = to_e4m3x2(u.x * f, u.y * f) | to_e4m3x2(v.x * f, v.y * f) << 16;
+        o[k] = to_e4m3x4(u.x * f, u.y * f, v.x * f, v.y * f);
       }
       *p = make_uint2(o[0], o[1]);
     }
   }
   if (lane == 0 && warp % W == 0) *scale = (uint8_t)e;
   const float f = exp2i(127 - e);
-  const bool cap = e >= kCapByte<E>;
+  const bool plain = e < kCapByte<E> && !odd;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int row = row0 + i * RPS;
     if (row < lo || row >= hi) continue;
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 y = Elem<E>::unpack(w[k]);
-      y.x *= f, y.y *= f;
-      if (cap) y.x = fminf(fmaxf(y.x, -240.f), 240.f), y.y = fminf(fmaxf(y.y, -240.f), 240.f);
-      if (odd) {  // (the conversion and the cap would make numbers of them)
-        if ((w[k] & 0x7FFFu) >= inf) y.x = __uint_as_float(0x7FC00000u);
-        if ((w[k] >> 16 & 0x7FFFu) >= inf) y.y = __uint_as_float(0x7FC00000u);
-      }
-      o[k] = to_e4m3x2(y.x, y.y);
-    }
-    *reinterpret_cast<uint2*>(dst + row * token_stride) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+    uint2* to = reinterpret_cast<uint2*>(dst + row * token_stride);
+    const float2 a0 = Elem<E>::unpack(x[i].x), a1 = Elem<E>::unpack(x[i].y), a2 = Elem<E>::unpack(x[i].z), a3 = Elem<E>::unpack(x[i].w);
+    *to = make_uint2(to_e4m3x4(a0.x * f, a0.y * f, a1.x * f, a1.y * f), to_e4m3x4(a2.x * f, a2.y * f, a3.x * f, a3.y * f));
+  }
+  if (plain) return;
+  // Once more for what the conversion does not do: no code past the type's range, NaN for what is not finite.
+  const float cap = e >= kCapByte<E> ? 240.f : 448.f;
+#pragma unroll 1
+  for (int z = 0; z < kSteps * 8; ++z) {
+    const int row = row0 + z / 8 * RPS;
+    if (row < lo || row >= hi) continue;
+    const float v = Elem<E>::unpack(static_cast<const uint16_t*>(values ? a.v : a.k)[(r.q0 + (block0 - r.ctx) + row) *
+                                        (values ? a.v_stride : a.k_stride) + (int64_t)head * D + e0 + z % 8]).x;
+    const float y = v - v == 0.f ? fminf(fmaxf(v * f, -cap), cap) : __uint_as_float(0x7FC00000u);
+    dst[row * token_stride + z % 8] = (uint8_t)to_e4m3x4(y, 0.f, 0.f, 0.f);
   }
 }
 

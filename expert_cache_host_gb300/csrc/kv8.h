@@ -40,13 +40,15 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) { return Elem<__half>::unpack(e4m3x2_to_f16x2(c)).x; }
 
-// Four e4m3 numbers times the power of two of scale byte e, rounded to a 16-bit
-// type, for the bytes whose factor that type holds.
+// Sixteen e4m3 numbers times the power of two of scale byte e, rounded to a 16-bit
+// type, for the bytes whose factor that type holds.  `sixteen` and `one` are these
+// numbers, unknown to the compiler: multiplications run beside the other pipe's
+// shifts and permutations, which bound this, and as shifts would join them.
 template <typename E>
 struct Scaled;
 template <>
 struct Scaled<__half> {
-  static __device__ __forceinline__ bool fast(uint32_t e, const uint4&) { return e - 103u <= 39u; }  // 2^-24 .. 2^15
+  static __device__ __forceinline__ bool fast(uint32_t e, uint32_t) { return e - 103u <= 39u; }  // 2^-24 .. 2^15
   static __device__ __forceinline__ uint32_t factor(uint32_t e) {
     const uint32_t f = e > 112u ? (e - 112u) << 10 : 1u << (e - 103u);
     return f * 0x10001u;
@@ -56,32 +58,43 @@ struct Scaled<__half> {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(f));
     return r;
   }
-  static __device__ __forceinline__ void four(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
-    lo = mul(e4m3x2_to_f16x2(w & 0xFFFFu), f);
-    hi = mul(e4m3x2_to_f16x2(w >> 16), f);
+  static __device__ __forceinline__ void convert(const uint4& v, uint32_t f, uint32_t, uint32_t, uint32_t* o, uint32_t&) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t lo, hi;
+      asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+          : "=r"(lo), "=r"(hi)
+          : "r"(w[k]));
+      o[2 * k] = mul(lo, f);
+      o[2 * k + 1] = mul(hi, f);
+    }
   }
 };
 template <>
 struct Scaled<__nv_bfloat16> {
   // A code's bits in a bf16's places (sign, the low exponent and the high fraction bits) are 2^-120 of it, but for NaN
-  // codes: 1 more changes their uppermost bit, and that of no others.
-  static __device__ __forceinline__ bool fast(uint32_t e, const uint4& v) {
-    constexpr uint32_t one = 0x01010101u;
-    const uint32_t nan = ((v.x + one) ^ v.x) | ((v.y + one) ^ v.y) | ((v.z + one) ^ v.z) | ((v.w + one) ^ v.w);
-    return e <= 134u && !(nan & 0x80808080u);
-  }
+  // codes: these and 1 have the uppermost bit of a byte (`nan`).
+  static __device__ __forceinline__ bool fast(uint32_t e, uint32_t nan) { return e <= 134u && !(nan & 0x80808080u); }
   static __device__ __forceinline__ uint32_t factor(uint32_t e) { return ((e + 120u) << 7) * 0x10001u; }  // 2^(e - 7)
   static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t f) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(f));
     return r;
   }
-  static __device__ __forceinline__ uint32_t place(uint32_t x) {  // codes in the upper bytes of the halves
-    return ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
-  }
-  static __device__ __forceinline__ void four(uint32_t w, uint32_t f, uint32_t& lo, uint32_t& hi) {
-    lo = mul(place(__byte_perm(w, 0, 0x1404)), f);
-    hi = mul(place(__byte_perm(w, 0, 0x3424)), f);
+  static __device__ __forceinline__ void convert(const uint4& v, uint32_t f, uint32_t sixteen, uint32_t one, uint32_t* o,
+                                                 uint32_t& nan) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t size = w[k] & 0x7F7F7F7Fu, sign = w[k] & 0x80808080u;
+      t[k] = size * one + 0x01010101u;
+      // halves of a size in the low byte, times 16, and the sign in the high one
+      o[2 * k] = mul(__byte_perm(size, 0, 0x4140) * sixteen + __byte_perm(sign, 0, 0x1404), f);
+      o[2 * k + 1] = mul(__byte_perm(size, 0, 0x4342) * sixteen + __byte_perm(sign, 0, 0x3424), f);
+    }
+    nan = (t[0] | t[1]) | (t[2] | t[3]);
   }
 };
 

@@ -65,6 +65,8 @@ extern "C" int ft_kv8_attention(const ft_kv8_attn_args* args, void* stream) {
   g.v_scale = args->cache.v_scale;
   g.log2_block = log2_of(args->cache.block_size);
   g.max_new = max_new;
+  g.sixteen = 16;
+  g.one = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) return args->dtype == FT_DTYPE_BF16 ? launch_few<__nv_bfloat16>(g, few, rows, st) : launch_few<__half>(g, few, rows, st);
   if (args->dtype == FT_DTYPE_BF16)

@@ -116,6 +116,7 @@ struct Args {
   // Q8: the cache's strides are bytes, and
   const uint8_t *k_scale, *v_scale;
   int log2_block, max_new;
+  uint32_t sixteen, one;  // as convert_rows wants them
 };
 
 // An item cut over several CTAs: parts = 0 where there is none.
@@ -445,7 +446,8 @@ __device__ __forceinline__ int64_t scale_index(const Args& g, int page, int in_p
 // bank.  The rows lie in two blocks at most: `bytes`, whose first 16 and last 16
 // rows' are warp-uniform.
 template <typename E, int D>
-__device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, uint32_t e_lo, uint32_t e_hi, int lane) {
+__device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, uint32_t e_lo, uint32_t e_hi, int lane,
+                                             uint32_t sixteen, uint32_t one) {
   constexpr int COLS = D / 64;  // passes over 8 rows
   // this lane's row of 8, and its columns in the first pass (in the second the others)
   const int row = D == 128 ? (lane >> 3) * 2 + ((lane >> 2) & 1) : lane >> 2;
@@ -472,15 +474,12 @@ __device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, u
     const uint32_t e = g < 2 ? e_lo : e_hi, f = Scaled<E>::factor(e);
 #pragma unroll
     for (int k = 0; k < COLS; ++k) {
-      uint32_t o[8];
-      Scaled<E>::four(v[k].x, f, o[0], o[1]);
-      Scaled<E>::four(v[k].y, f, o[2], o[3]);
-      Scaled<E>::four(v[k].z, f, o[4], o[5]);
-      Scaled<E>::four(v[k].w, f, o[6], o[7]);
+      uint32_t o[8], nan = 0;
+      Scaled<E>::convert(v[k], f, sixteen, one, o, nan);
       uint8_t* to = out + (COLS == 2 ? (half ^ k) * (128 * 128) : 0);
       *reinterpret_cast<uint4*>(to + lo) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(to + hi) = make_uint4(o[4], o[5], o[6], o[7]);
-      if (!Scaled<E>::fast(e, v[k])) {
+      if (!Scaled<E>::fast(e, nan)) {
         const float scale = scale_of(e);
         const uint8_t* from = in - 8 * D + (COLS == 2 ? (half ^ k) * 64 : 0);
 #pragma unroll 1
@@ -667,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             const uint32_t pages = sh.raw_pages[st8];
             convert_rows<E, D>(ring8 + st8 * C::TILE8 + first_row * D, ring + st * C::TILE + first_row * 128,
                                uniform(sh.raw_scale[st8][first_row >> g.log2_block]),
-                               uniform(sh.raw_scale[st8][(first_row + 16) >> g.log2_block]), lane);
+                               uniform(sh.raw_scale[st8][(first_row + 16) >> g.log2_block]), lane, g.sixteen, g.one);
             if (kv && special(t, pages)) {
               const int left = wk.r.ctx + wk.r.n - t * KT;
               __syncwarp();

@@ -59,7 +59,7 @@ extern "C" int ft_kv8_attention(const ft_kv8_attn_args* args, void* stream) {
   const int max_new = args->max_new ? std::min(args->max_new, a.max_tokens) : a.max_tokens;
   // Few rows: a kernel whose products take 8 or 16, on two CTAs or one an SM.
   const int64_t rows = (int64_t)max_new * (a.q_heads / a.cache.kv_heads);
-  const int few = rows <= 8 ? 2 * grid : rows <= 16 ? grid : 0;
+  const int few = rows > 16 ? 0 : rows <= 8 || D == 64 ? 2 * grid : grid;
   Args g = few ? make_args(a, few, kv8_few::kRows) : make_args(a, grid);
   g.k_scale = args->cache.k_scale;
   g.v_scale = args->cache.v_scale;

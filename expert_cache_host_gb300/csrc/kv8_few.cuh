@@ -49,11 +49,14 @@ constexpr float kUp = 11.f, kLagP = 4.f, kLagL = 8.f;  // P <= 2^15, p <= 2^8
 template <int D, int NB>
 struct Cfg {
   static constexpr int R = 8 * NB;                        // rows
-  static constexpr int CTAS = NB == 1 ? 2 : 1;            // of an SM
+  static constexpr int CTAS = NB == 1 || D == 64 ? 2 : 1;  // of an SM: what the registers allow
   static constexpr int HALF = kChunk * D;                 // bytes of a chunk's keys or values
-  static constexpr int STAGES = NB == 1 && D == 128 ? 3 : 4;
+  // Two chunks a warp: with three, 128 KB of an SM in flight, 64 requests of 16384 keys took 184 us in place of 174 (and 95
+  // in place of 89 of the ragged ones).
+  static constexpr int STAGES = 2;
   static constexpr int RING = kWarps * STAGES * 2 * HALF;
-  static constexpr int JOIN = kWarps * D * R * 4;         // the warps' outputs, in the ring's place
+  static constexpr int LINE = D + 4;                      // floats of a row's output: rows 2 t4 apart by 8 banks
+  static constexpr int JOIN = kWarps * R * LINE * 4;      // the warps' outputs, in the ring's place
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;  // and Shared
 };
 
@@ -133,38 +136,80 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     const Req& r = wk.r;
     const int keys = r.ctx + r.n, rows = r.n * g.G, tiles = wk.t1 - wk.t0;
     const int32_t* table = a.block_table + (int64_t)wk.b * a.table_width;
-    // The page of the warp's chunk of tile t; -1: none.
-    auto page_of = [&](int t) {
-      const int key0 = t * KT + warp * kChunk, col = key0 >> g.log2_page;
-      return t < wk.t1 && key0 < keys && col < a.table_width ? table[col] : -1;
-    };
-    int page = page_of(wk.t0);
+    // Queries, as the lane's numbers come in K's: D / 4 from D / 4 t4 on (loaded before the pages are known).
+    uint4 qw[NB][D / 32];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = nb * 8 + gid, i = row / g.G;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) qw[nb][k] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (r.q0 + i) * a.q_stride + (int64_t)(wk.h * g.G + row - i * g.G) * D;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) qw[nb][k] = *reinterpret_cast<const uint4*>(q + t4 * (D / 4) + k * 8);
+      }
+    }
 
-    // Queries, as the lane's numbers come in K's: D / 4 from D / 4 t4 on.
+    // A window of 32 tiles: lane i has the page of the warp's chunk of tile `window` + i, and its scale bytes (or that
+    // there is none).  The next window's are fetched on the way through this one, the last one's bytes kept for the
+    // chunks that are still to be read.
+    constexpr uint32_t kNone = 1u << 16;
+    int window = wk.t0, window_read = wk.t0;
+    auto page_at = [&](int first) {  // of tile first + lane; -1: none
+      const int key0 = (first + lane) * KT + warp * kChunk, col = key0 >> g.log2_page;
+      if (first + lane >= wk.t1 || key0 >= keys) return -1;
+      const int pg = col < a.table_width ? table[col] : -1;
+      if (pg >= 0 && pg < a.cache.num_pages) return pg;
+      if (a.status) atomicOr(a.status, FT_ST_BAD_SLOT);
+      return -1;
+    };
+    auto bytes_at = [&](int first, int pg) -> uint32_t {
+      if (pg < 0) return kNone;
+      const int64_t at = tree_attention::scale_index(g, pg, ((first + lane) * KT + warp * kChunk) & page_mask, wk.h);
+      return __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
+    };
+    int page = page_at(wk.t0), page_next = -1;
+    uint32_t bytes = bytes_at(wk.t0, page), bytes_next = kNone;
+    // The warp's chunk of tile t on its way into stage st.
+    auto issue = [&](int t, int st) {
+      if (t >= wk.t1) return;
+      if (t == window + 16) page_next = page_at(window + 32);
+      if (t == window + 24) bytes_next = bytes_at(window + 32, page_next);
+      if (t == window + 32) window = t, page = page_next;
+      const int pg = __shfl_sync(~0u, page, t - window), row0 = (t * KT + warp * kChunk) & page_mask;
+      if (pg < 0 || late) return;
+      if (lane == 0) {
+        mbar_expect_tx(&sh.full[warp][st], 2 * C::HALF);
+        tensor_g2s_4d(ring + st * 2 * C::HALF, &map_k, 0, row0, wk.h, pg, &sh.full[warp][st]);
+        tensor_g2s_4d(ring + st * 2 * C::HALF + C::HALF, &map_v, 0, row0, wk.h, pg, &sh.full[warp][st]);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < S; ++k) issue(wk.t0 + k, k);
+
     uint32_t qf[NB][KS][2];
     int qe[NB];  // q = qf * 2^-qe
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int row = nb * 8 + gid, i = row / g.G;
-      uint4 w[D / 32];
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) w[k] = make_uint4(0, 0, 0, 0);
-      if (row < rows) {
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (r.q0 + i) * a.q_stride + (int64_t)(wk.h * g.G + row - i * g.G) * D;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          w[k] = *reinterpret_cast<const uint4*>(q + t4 * (D / 4) + k * 8);
-      }
       uint32_t u[D / 8];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) u[4 * k] = w[k].x, u[4 * k + 1] = w[k].y, u[4 * k + 2] = w[k].z, u[4 * k + 3] = w[k].w;
+      for (int k = 0; k < D / 32; ++k) u[4 * k] = qw[nb][k].x, u[4 * k + 1] = qw[nb][k].y, u[4 * k + 2] = qw[nb][k].z, u[4 * k + 3] = qw[nb][k].w;
       qe[nb] = 0;
       if constexpr (BF) {
-        uint32_t most = 0;  // the largest finite number's bits
+        uint32_t two = 0;
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint32_t x = u[k] & 0x7FFFu, y = u[k] >> 16 & 0x7FFFu;
-          most = max(most, max(x < 0x7F80u ? x : 0u, y < 0x7F80u ? y : 0u));
+        for (int k = 0; k < D / 8; ++k) two = max_abs2<E>(two, u[k]);
+        two &= 0x7FFF7FFFu;
+        uint32_t most = max(two & 0xFFFFu, two >> 16);  // the largest number's bits
+        if (most >= 0x7F80u) {                          // (of the finite ones)
+          most = 0;
+#pragma unroll 1
+          for (int k = 0; k < D / 4; ++k) {
+            const int row = nb * 8 + gid, i = row / g.G;
+            const uint32_t x = static_cast<const uint16_t*>(a.q)[(r.q0 + i) * a.q_stride +
+                                                                (int64_t)(wk.h * g.G + row - i * g.G) * D + t4 * (D / 4) + k] & 0x7FFFu;
+            if (x < 0x7F80u) most = max(most, x);
+          }
         }
         most = max(most, __shfl_xor_sync(~0u, most, 1));
         most = max(most, __shfl_xor_sync(~0u, most, 2));
@@ -199,33 +244,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
       }
     }
 
-    // The warp's chunk of tile t on its way into stage st; returns its scale bytes, or that there is none.
-    constexpr uint32_t kNone = 1u << 16;
-    auto issue = [&](int t, int st, int pg) -> uint32_t {
-      const int key0 = t * KT + warp * kChunk;
-      if (t >= wk.t1 || key0 >= keys || late) return kNone;
-      if (pg < 0 || pg >= a.cache.num_pages) {
-        if (a.status && lane == 0) atomicOr(a.status, FT_ST_BAD_SLOT);
-        return kNone;
-      }
-      const int row0 = key0 & page_mask;
-      if (lane == 0) {
-        mbar_expect_tx(&sh.full[warp][st], 2 * C::HALF);
-        tensor_g2s_4d(ring + st * 2 * C::HALF, &map_k, 0, row0, wk.h, pg, &sh.full[warp][st]);
-        tensor_g2s_4d(ring + st * 2 * C::HALF + C::HALF, &map_v, 0, row0, wk.h, pg, &sh.full[warp][st]);
-      }
-      const int64_t at = tree_attention::scale_index(g, pg, row0, wk.h);
-      return __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
-    };
-
-    uint32_t meta[S];  // the next chunks' scale bytes
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int after = page_of(wk.t0 + k + 1);
-      meta[k] = issue(wk.t0 + k, k, page);
-      page = after;
-    }
-
     // A row's maximum and offset as they are and (0 where there is none yet) as they are used.
     float M[NB][2], mo[NB][2], l[NB][2], Mr[NB][2], up[NB][2];
     float o[MT][NB][4];
@@ -245,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
 #pragma unroll 1
     for (int n = 0; n < tiles; ++n) {
       const int t = wk.t0 + n, key0 = t * KT + warp * kChunk;
-      const uint32_t bytes = meta[0];
-      if (!(bytes & kNone)) {
+      if (t == window_read + 32) window_read = t, bytes = bytes_next;
+      const uint32_t scales = __shfl_sync(~0u, bytes, t - window_read);
+      if (!(scales & kNone)) {
         if (__any_sync(~0u, !mbar_wait(&sh.full[warp][st], parity >> st & 1, late))) late = true;
         parity ^= 1u << st;
         const uint8_t* kc = ring + st * 2 * C::HALF;
@@ -270,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
             for (int nb = 0; nb < NB; ++nb) mma(x[nb], a0, a1, a2, a3, qf[nb][k * 4 + w][0], qf[nb][k * 4 + w][1]);
           }
         }
-        const uint32_t ek = bytes & 255u, ev = bytes >> 8 & 255u;
+        const uint32_t ek = scales & 255u, ev = scales >> 8 & 255u;
         const float kf = scale_of(ek), shift = ev == 255u ? 0.f : (float)((int)ev - 127);
         const bool special = key0 + kChunk > r.ctx;  // new keys, or rows past the end
         uint32_t seen[NB][2];                        // the row's keys of the chunk
@@ -410,16 +429,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
       }
       proxy_fence_reads();
       __syncwarp();
-      const int after = page_of(t + S + 1);
-      const uint32_t next = issue(t + S, st, page);
-      page = after;
-#pragma unroll
-      for (int k = 0; k + 1 < S; ++k) meta[k] = meta[k + 1];
-      meta[S - 1] = next;
+      issue(t + S, st);
       if (++st == S) st = 0;
     }
 
-    // The warps' sums joined: in the rings' place, [warp][number of a lane][gid][row].
+    // The warps' sums joined: in the rings' place, [warp][row][pair of a lane][gid][2].
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -438,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     for (int k = 0; k < MT; ++k) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float* to = outs + ((warp * (D / 8) + 2 * k) * 8 + gid) * R + nb * 8 + 2 * t4;
-        *reinterpret_cast<float2*>(to) = make_float2(o[k][nb][0], o[k][nb][1]);
-        *reinterpret_cast<float2*>(to + 8 * R) = make_float2(o[k][nb][2], o[k][nb][3]);
+        float* to = outs + (warp * R + nb * 8 + 2 * t4) * C::LINE + k * 16 + gid * 2;
+        *reinterpret_cast<float2*>(to) = make_float2(o[k][nb][0], o[k][nb][2]);
+        *reinterpret_cast<float2*>(to + C::LINE) = make_float2(o[k][nb][1], o[k][nb][3]);
       }
     }
     if (tid < R) {
@@ -461,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
         const float mw = sh.m[w][tid], down = mw == -CUDART_INF_F ? 0.f : (mw - m) * g.c;
         const bool some = mw != -CUDART_INF_F || sh.l[w][tid] != 0.f;
         const float at = sh.mo[w][tid] == -CUDART_INF_F ? 0.f : sh.mo[w][tid] + down - off;
-        sh.f[w][tid] = some ? ex2(at) : 0.f;
+        sh.f[w][tid] = some ? ex2(at) : -1.f;  // (-1: nothing to add)
       }
       sh.most[tid] = m;
       sh.sum[tid] = sum;
@@ -471,33 +485,36 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     const bool whole = wk.t0 == 0 && wk.t1 == r.tiles;
     const int slot = blockIdx.x * 2 + (wk.t0 == 0 ? 1 : 0);
     for (int z = tid; z < rows * (D / 4); z += kThreads) {
-      const int col = z / rows, row = z - col * rows;
+      const int row = z / (D / 4), quad = z % (D / 4);
       float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = sh.f[w][row];
-        if (f == 0.f) continue;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int d = col * 4 + k;
-          y[k] += f * outs[((w * (D / 8) + d % (D / 8)) * 8 + d / (D / 8)) * R + row];
-        }
+        const float4 x = *reinterpret_cast<const float4*>(outs + (w * R + row) * C::LINE + quad * 4);
+        if (f == -1.f) continue;
+        y[0] += f * x.x, y[1] += f * x.y, y[2] += f * x.z, y[3] += f * x.w;
       }
       const float sum = sh.sum[row], norm = sh.norm[row];
       const bool some = sum > 0.f || sum != sum;
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] = some ? y[k] * norm / sum * norm : 0.f;
       const int i = row / g.G, head = wk.h * g.G + row - i * g.G;
-      if (whole) {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (r.q0 + i) * a.out_stride + (int64_t)head * D + col * 4) =
-            make_uint2(Elem<E>::pack(y[0], y[1]), Elem<E>::pack(y[2], y[3]));
-        if (a.lse && col == 0)
-          a.lse[(int64_t)(r.q0 + i) * a.q_heads + head] = some ? (sh.most[row] * g.c + log2f(sum)) * kLn2 : -CUDART_INF_F;
-      } else {
-        g.part_o[((int64_t)slot * (D / 4) + col) * kRows + row] = make_float4(y[0], y[1], y[2], y[3]);
-        if (col == 0)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // two neighbours of one lane, and of the next
+        const int d = (quad % 4 * 2 + k) * (D / 8) + quad / 4 * 2;
+        if (whole)
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (r.q0 + i) * a.out_stride + (int64_t)head * D + d) =
+              Elem<E>::pack(y[2 * k], y[2 * k + 1]);
+        else
+          reinterpret_cast<float2*>(g.part_o + ((int64_t)slot * (D / 4) + d / 4) * kRows + row)[d / 2 % 2] =
+              make_float2(y[2 * k], y[2 * k + 1]);
+      }
+      if (quad == 0) {
+        if (!whole)
           g.part_ml[slot * kRows + row] =
               make_float2(some ? sh.most[row] : -CUDART_INF_F, sum * (Held<E>::kUp == 0.f ? 1.f : 2048.f));
+        else if (a.lse)
+          a.lse[(int64_t)(r.q0 + i) * a.q_heads + head] = some ? (sh.most[row] * g.c + log2f(sum)) * kLn2 : -CUDART_INF_F;
       }
     }
     if (!whole && wk.t0 == 0) {

@@ -32,6 +32,10 @@ def ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
 class Model:
     def __init__(self, seed):
         g = torch.Generator(device="cuda").manual_seed(seed)
@@ -65,35 +69,37 @@ class Engine:
         self.m, self.B = model, len(prompts)
         self.said = [list(p) for p in prompts]  # the last token of each is not in the cache yet
         self.ctx = [0] * self.B
-        self.k, self.v = (torch.zeros((L, pages, PAGE, HKV, HEAD), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        self.make_cache(pages)
         self.table = torch.full((self.B, MAX_POS // PAGE), -1, dtype=torch.int32, device="cuda")
         self.free = list(range(pages))
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.workspace = None
 
+    def make_cache(self, pages):
+        self.k, self.v = (torch.zeros((L, pages, PAGE, HKV, HEAD), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
     def plan(self, args, mask, st):
         """Lays the step out; `mask` is the tensor behind args.mask."""
         ft.ft_kv_plan(args, st)
 
-    def step(self, tokens, parents, given=None):
-        """One pass over each request's new tokens (parents: None where they follow one another).  Returns the plan's
-        slots and, for every row, its most likely token, that token's log probability, and the log probability of
-        given[row] (NaN where that is -1; None without `given`)."""
+    def forward(self, tokens, parents):
+        """One pass over each request's new tokens (parents: None where they follow one another).  Returns the plan and
+        the logits of every row."""
         new = [len(t) for t in tokens]
         T, st = sum(new), torch.cuda.current_stream().cuda_stream
-        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
         flat, ctx_len, new_len = i32(sum(tokens, [])), i32(self.ctx), i32(new)
         tree = parents is not None
         par = i32(sum(parents, [])) if tree else None
         stack, count, left = i32(self.free), i32([len(self.free)]), i32([0])
-        q_start, positions = i32([0] * (self.B + 1)), i32([0] * T)
-        slots = torch.empty(T, dtype=torch.int64, device="cuda")
-        mask = torch.zeros((T, WORDS), dtype=torch.int32, device="cuda") if tree else None
+        p = argparse.Namespace(T=T, st=st, tokens=flat, parents=par, ctx_len=ctx_len, longest=max(new), words=WORDS if tree else 0,
+                               q_start=i32([0] * (self.B + 1)), positions=i32([0] * T),
+                               slots=torch.empty(T, dtype=torch.int64, device="cuda"),
+                               mask=torch.zeros((T, WORDS), dtype=torch.int32, device="cuda") if tree else None)
         self.plan(ft.make_plan_args(
             ctx_len=ptr(ctx_len), new_len=ptr(new_len), parents=ptr(par), free_pages=ptr(stack), free_count=ptr(count),
-            block_table=ptr(self.table), q_start=ptr(q_start), slots=ptr(slots), positions=ptr(positions), mask=ptr(mask),
-            free_left=ptr(left), status=ptr(self.status), num_reqs=self.B, page_size=PAGE,
-            table_width=self.table.shape[1], max_tokens=T, mask_words=WORDS if tree else 0), mask, st)
+            block_table=ptr(self.table), q_start=ptr(p.q_start), slots=ptr(p.slots), positions=ptr(p.positions),
+            mask=ptr(p.mask), free_left=ptr(left), status=ptr(self.status), num_reqs=self.B, page_size=PAGE,
+            table_width=self.table.shape[1], max_tokens=T, mask_words=p.words), p.mask, st)
         x = self.m.embed[flat.long()].float()
         q = torch.empty((T, HQ * HEAD), dtype=torch.bfloat16, device="cuda")
         att = torch.empty_like(q)
@@ -101,44 +107,62 @@ class Engine:
         for l in range(L):
             h = norm(x)
             qkv = h @ self.m.qkv[l]
-            cache = ft.make_kv_cache(
-                k=ptr(self.k[l]), v=ptr(self.v[l]), dtype=ft.FT_DTYPE_BF16, num_pages=self.k.shape[1], page_size=PAGE,
-                kv_heads=HKV, head_dim=HEAD, k_page_stride=PAGE * HKV * HEAD, k_token_stride=HKV * HEAD,
-                k_head_stride=HEAD, v_page_stride=PAGE * HKV * HEAD, v_token_stride=HKV * HEAD, v_head_stride=HEAD)
-            ld = qkv.stride(0)
-            ft.ft_qk_norm_rope(ft.make_qk_args(
-                q=ptr(qkv), k=ptr(qkv) + 2 * HQ * HEAD, v=ptr(qkv) + 2 * (HQ + HKV) * HEAD, q_weight=ptr(self.m.q_norm[l]),
-                k_weight=ptr(self.m.k_norm[l]), cos_sin=ptr(self.m.cos_sin), positions=ptr(positions), slots=ptr(slots),
-                q_out=ptr(q), status=ptr(self.status), q_stride=ld, k_stride=ld, v_stride=ld, q_out_stride=HQ * HEAD, T=T,
-                q_heads=HQ, rot_dim=HEAD, max_pos=MAX_POS, interleaved=0, eps=1e-6, cache=cache), st)
-            args = ft.make_attn_args(
-                q=ptr(q), out=ptr(att), q_start=ptr(q_start), ctx_len=ptr(ctx_len), block_table=ptr(self.table),
-                mask=ptr(mask), status=ptr(self.status), q_stride=HQ * HEAD, out_stride=HQ * HEAD, max_tokens=T,
-                num_reqs=self.B, q_heads=HQ, table_width=self.table.shape[1], mask_words=WORDS if tree else 0,
-                scale=HEAD ** -0.5, cache=cache)
-            if self.workspace is None:
-                self.workspace = torch.empty(ft.ft_tree_attention_workspace(args), dtype=torch.uint8, device="cuda")
-            args.workspace, args.workspace_bytes = ptr(self.workspace), self.workspace.numel()
-            ft.ft_tree_attention(args, st)
+            self.attend(l, p, qkv, q, att)
             x = x + (att @ self.m.o[l]).float()
             h = norm(x)
             logits = (h.float() @ self.m.router[l]).contiguous()
             ft.ft_cache_step(self.m.ctx, l, ptr(logits), T, st)
             ft.ft_moe_forward(self.m.ctx, l, ft.FT_DECODE_CACHED, 0, ptr(h), T, 0, ptr(y), st)
             x = x + y
-        logits = norm(x) @ self.m.head
-        best = torch.empty((T, 1), dtype=torch.int32, device="cuda")
-        best_lp = torch.empty((T, 1), dtype=torch.float32, device="cuda")
-        entropy = torch.empty(T, dtype=torch.float32, device="cuda")
-        asked = None if given is None else i32(given)
-        given_lp = None if given is None else torch.empty(T, dtype=torch.float32, device="cuda")
-        ft.ft_token_logprobs(ft.make_logprob_args(
-            logits=ptr(logits), tokens=ptr(asked), logprob=ptr(given_lp), entropy=ptr(entropy), top_ids=ptr(best), top_logprobs=ptr(best_lp), status=ptr(self.status),
-            row_stride=logits.stride(0), dtype=ft.FT_DTYPE_BF16, T=T, V=VOCAB, top_n=1), st)
         self.free = self.free[:int(left.item())]
+        return p, norm(x) @ self.m.head
+
+    def queries_and_keys(self, l, p, qkv, q, cache, slots):
+        """Norms and rotation; queries to q, keys and values to `slots` of `cache`."""
+        ld = qkv.stride(0)
+        ft.ft_qk_norm_rope(ft.make_qk_args(
+            q=ptr(qkv), k=ptr(qkv) + 2 * HQ * HEAD, v=ptr(qkv) + 2 * (HQ + HKV) * HEAD, q_weight=ptr(self.m.q_norm[l]),
+            k_weight=ptr(self.m.k_norm[l]), cos_sin=ptr(self.m.cos_sin), positions=ptr(p.positions), slots=ptr(slots),
+            q_out=ptr(q), status=ptr(self.status), q_stride=ld, k_stride=ld, v_stride=ld, q_out_stride=HQ * HEAD, T=p.T,
+            q_heads=HQ, rot_dim=HEAD, max_pos=MAX_POS, interleaved=0, eps=1e-6, cache=cache), p.st)
+
+    def attend(self, l, p, qkv, q, att):
+        """Layer l's attention of the step's rows."""
+        cache = ft.make_kv_cache(
+            k=ptr(self.k[l]), v=ptr(self.v[l]), dtype=ft.FT_DTYPE_BF16, num_pages=self.k.shape[1], page_size=PAGE,
+            kv_heads=HKV, head_dim=HEAD, k_page_stride=PAGE * HKV * HEAD, k_token_stride=HKV * HEAD,
+            k_head_stride=HEAD, v_page_stride=PAGE * HKV * HEAD, v_token_stride=HKV * HEAD, v_head_stride=HEAD)
+        self.queries_and_keys(l, p, qkv, q, cache, p.slots)
+        args = ft.make_attn_args(
+            q=ptr(q), out=ptr(att), q_start=ptr(p.q_start), ctx_len=ptr(p.ctx_len), block_table=ptr(self.table),
+            mask=ptr(p.mask), status=ptr(self.status), q_stride=HQ * HEAD, out_stride=HQ * HEAD, max_tokens=p.T,
+            num_reqs=self.B, q_heads=HQ, table_width=self.table.shape[1], mask_words=p.words,
+            scale=HEAD ** -0.5, cache=cache)
+        if self.workspace is None:
+            self.workspace = torch.empty(ft.ft_tree_attention_workspace(args), dtype=torch.uint8, device="cuda")
+        args.workspace, args.workspace_bytes = ptr(self.workspace), self.workspace.numel()
+        ft.ft_tree_attention(args, p.st)
+
+    def check(self):
         if int(self.status.item()) or ft.ft_get_status(self.m.ctx):
             raise RuntimeError(f"device status {int(self.status.item())}")
-        return slots, best[:, 0].tolist(), best_lp[:, 0].tolist(), None if given is None else given_lp.tolist()
+
+    def step(self, tokens, parents, given=None):
+        """One pass over each request's new tokens (parents: None where they follow one another).  Returns the plan's
+        slots and, for every row, its most likely token, that token's log probability, and the log probability of
+        given[row] (NaN where that is -1; None without `given`)."""
+        p, logits = self.forward(tokens, parents)
+        best = torch.empty((p.T, 1), dtype=torch.int32, device="cuda")
+        best_lp = torch.empty((p.T, 1), dtype=torch.float32, device="cuda")
+        entropy = torch.empty(p.T, dtype=torch.float32, device="cuda")
+        asked = None if given is None else i32(given)
+        given_lp = None if given is None else torch.empty(p.T, dtype=torch.float32, device="cuda")
+        ft.ft_token_logprobs(ft.make_logprob_args(
+            logits=ptr(logits), tokens=ptr(asked), logprob=ptr(given_lp), entropy=ptr(entropy), top_ids=ptr(best),
+            top_logprobs=ptr(best_lp), status=ptr(self.status), row_stride=logits.stride(0), dtype=ft.FT_DTYPE_BF16, T=p.T,
+            V=VOCAB, top_n=1), p.st)
+        self.check()
+        return p.slots, best[:, 0].tolist(), best_lp[:, 0].tolist(), None if given is None else given_lp.tolist()
 
     def keep(self, b, slots, path, new):
         """Keep the new tokens `path` (indices, ascending) of request b: their keys and values move to the places
@@ -148,7 +172,11 @@ class Engine:
         for c in (self.k, self.v):
             rows = c.view(L, -1, HKV, HEAD)
             rows[:, dst] = rows[:, src].clone()
-        was, self.ctx[b] = self.ctx[b], self.ctx[b] + len(path)
+        self.advance(b, len(path), new)
+
+    def advance(self, b, kept, new):
+        """`kept` of request b's `new` tokens belong to its context now."""
+        was, self.ctx[b] = self.ctx[b], self.ctx[b] + kept
         held = -(-self.ctx[b] // PAGE)
         self.free += reversed(self.table[b, held:max(held, -(-(was + new) // PAGE))].tolist())
 

@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     constexpr uint32_t kNone = 1u << 16;
     int window = wk.t0, window_read = wk.t0;
     auto page_at = [&](int first) {  // of tile first + lane; -1: none
+      if (first + lane >= wk.t1) return -1;
       const int key0 = (first + lane) * KT + warp * kChunk, col = key0 >> g.log2_page;
-      if (first + lane >= wk.t1 || key0 >= keys) return -1;
+      if (key0 >= keys) return -1;
       const int pg = col < a.table_width ? table[col] : -1;
       if (pg >= 0 && pg < a.cache.num_pages) return pg;
       if (a.status) atomicOr(a.status, FT_ST_BAD_SLOT);

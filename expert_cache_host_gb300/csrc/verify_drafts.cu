@@ -42,10 +42,11 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRejected = 64;
 constexpr int kUnit = 45;  // sums are in units of 2^-45
-constexpr int kNumbers = 8;  // of a thread in a round
-constexpr int kDepth = 3;    // rounds on their way
-constexpr int kResident = 4;  // CTAs of an SM
-constexpr int kPieces = 64;  // of a warp's stretch at most: a round each, or several
+constexpr int kNumbers = 16;  // of a thread in a round
+constexpr int kDepth = 2;     // rounds on their way
+constexpr int kResident = 2;   // CTAs of an SM
+constexpr int kPieces = 64;    // of a warp's stretch at most
+constexpr int kPiece = 4;      // rounds of a piece, or a multiple
 
 template <typename E>
 struct Prob {  // a 16-byte vector of a row
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
     const int base = (vec ? r.off : 0) - N;  // first element of group 0
     // A lane takes every 32nd vector of its warp's stretch, kVecs of them a round.
     constexpr int kVecs = kNumbers / N;
-    const int rounds = (per + 32 * kVecs - 1) / (32 * kVecs), piece = (rounds + kPieces - 1) / kPieces;
+    const int rounds = (per + 32 * kVecs - 1) / (32 * kVecs), piece = (rounds + kPieces * kPiece - 1) / (kPieces * kPiece) * kPiece;
     const int limit = base + g1 * N;  // of the stretch
     auto first_of = [&](int round, int v) { return base + (g0 + (round * kVecs + v) * 32 + lane) * N; };
     auto copy = [&](int round) {
@@ -399,24 +400,30 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
       auto pass = [&](auto how) {
         uint64_t piece_sum = 0;
         int left = piece, at = 0;
+        Levels sum;
+        uint32_t count = 0;
 #pragma unroll 1
         for (int i = 0; i < kDepth; ++i) copy(i);
 #pragma unroll 1
         for (int round = 0; round < rounds; ++round) {
           copy_wait<kDepth - 1>();
-          Levels sum;
           uint64_t hi[kNumbers / 2], lo[kNumbers / 2];
           weights(how, round, hi, lo);
 #pragma unroll
           for (int i = 0; i < kNumbers / 2; ++i) sum.add(hi[i], lo[i]);
+          count += kNumbers;
           copy(round + kDepth);
-          sum.finish(kNumbers);
+          if ((round + 1) % kPiece != 0 && round + 1 != rounds) continue;
+          sum.finish(count);
           // (the first level's number in two parts: a warp's could pass 32 bits)
           const uint32_t up = __reduce_add_sync(~0u, sum.a >> 12), low = __reduce_add_sync(~0u, sum.a & 0xFFFu);
           const int32_t rest = __reduce_add_sync(~0u, (int32_t)sum.b);
           piece_sum += ((((uint64_t)up << 12) + low) << (kUnit - 22)) + (int64_t)rest;
           size += (float)up * 0x1p-10f;
-          if (--left == 0 || round + 1 == rounds) {
+          sum = Levels();
+          count = 0;
+          left -= kPiece;
+          if (left == 0 || round + 1 == rounds) {
             if (lane == 0) sh.piece[warp][at] = piece_sum;
             whole_sum += piece_sum;
             piece_sum = 0;
@@ -583,11 +590,12 @@ cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
 
 template <typename E>
 cudaError_t launch_cs(const ft_verify_args& a, cudaStream_t st) {
-  // As many CTAs a request as run at once, while a lane has more than one vector of a row.  (A cluster lies in one GPC:
-  // of 16 CTAs they leave a sixth of the places empty and more.  37 requests of 50021 16-bit entries 23 us with 16, 18 with 8.)
+  // As many CTAs a request as run at once, while a lane has more than one vector of a row.  A cluster lies in one GPC, so
+  // of 16 CTAs there is room for two on every 18 SMs (16 requests of 131072 entries: 17.5 us with 16, 22.3 with 8; with a
+  // cluster more than there is room for, 37 requests of 50021 16-bit entries took 23 us, with 8 CTAs each 18).
   int cs = 1;
-  while (cs < kMaxCluster && (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * (cs < 8 ? kResident : 2) &&
-         a.V / Prob<E>::N / cs > kThreads)
+  while (cs < kMaxCluster && a.V / Prob<E>::N / cs > kThreads &&
+         (cs < 8 ? (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident : (int64_t)a.num_reqs * 9 <= sm_count()))
     cs *= 2;
   switch (cs) {
     case 1: return launch<E, 1>(a, st);

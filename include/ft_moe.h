@@ -71,12 +71,14 @@ extern "C" {
 
 /* device status bits (ft_get_status) */
 #define FT_ST_ROUTE_RANGE 1u /* a route id was outside [0, E) */
-#define FT_ST_NAN 2u         /* a router logit was NaN */
+#define FT_ST_NAN 2u         /* a router logit was NaN (attention side: a logit, probability or scale out of range) */
 #define FT_ST_CLOCK_WRAP 4u  /* the LRU step clock reached 2^32 - 1 */
 #define FT_ST_BAD_SLOT 8u    /* a slot id outside [0, S) reached a kernel */
 #define FT_ST_TIMEOUT 16u    /* a bounded wait for an asynchronous copy ran out; the kernel exited early */
-#define FT_ST_NO_ROOM 32u    /* ft_kv_plan: free pages, block-table columns or token rows ran out, or a length was negative */
-#define FT_ST_BAD_TREE 64u   /* a drafted token's parent was not an earlier token of its request, or the tree exceeded mask_words */
+#define FT_ST_NO_ROOM 32u    /* ft_kv_plan: free pages, block-table columns or token rows ran out, or a length was negative;
+                              * ft_kv8_attention: a request had more new tokens than max_new */
+#define FT_ST_BAD_TREE 64u   /* a drafted token's parent was not an earlier token of its request, or the tree exceeded mask_words;
+                              * ft_verify_drafts: more children of a row were rejected than are kept */
 #define FT_ST_BAD_TOKEN 128u /* a token id outside [0, V) or a position outside [0, max_pos) */
 
 #define FT_DTYPE_BF16 0

@@ -1,5 +1,6 @@
-// Attention of a step's tokens over the paged cache (ft_tree_attention) on the
-// fifth-generation tensor cores.
+// Attention of a step's tokens over the paged cache on the fifth-generation tensor
+// cores: ft_tree_attention, and (Q8) ft_kv8_attention where a request has more than
+// a few rows.
 //
 // For one request and key head, the rows that read the same keys are the
 // step's tokens times the query heads of the group (r = token * G + head).  A
@@ -43,6 +44,18 @@
 // non-finite new value adds it in the epilogue.  Only tiles that can hold such
 // rows go through warp 10: their V lands on the stage's `raw` barrier, and the
 // warp passes it on to `full`.
+//
+// Q8: tiles come as 8-bit codes through a ring of their own, and four more warps
+// turn them into the 16-bit tiles of the products (code * 2^(e-127), exact but for
+// f16's numbers below 2^-14; V's rows are looked over by them too).  The two
+// products, not the bytes, then bound long trees: 32 of 24..32 tokens over 8K..32K
+// keys, 0.69 GB, 0.30 TFLOP, take 385 us in bf16 and 341 in f16, where the 16-bit
+// cache takes 254 and no conversion at all took 325.  What the conversion costs is
+// the pipe of shifts, permutations and 8-bit conversions, 2 cycles a warp
+// instruction: f16 takes one conversion a pair of codes, bf16, for which there is
+// none, 3.3 such instructions and 1.3 on the multipliers' pipe (4 and more before:
+// 428 us), beside the softmax warps' own.  In shared memory a tile is written
+// twice and read twice, 1000 cycles besides the products' 1500.
 #pragma once
 
 #include <math_constants.h>

@@ -48,9 +48,10 @@ template <typename E>
 struct Scaled;
 template <>
 struct Scaled<__half> {
-  static __device__ __forceinline__ bool fast(uint32_t e, uint32_t) { return e - 103u <= 39u; }  // 2^-24 .. 2^15
+  // 2^-24 .. 2^15, and 0 where 448 * 2^(e - 127) rounds to it (blocks of zeros, places without a block).
+  static __device__ __forceinline__ bool fast(uint32_t e, uint32_t) { return e - 103u <= 39u || e <= 93u; }
   static __device__ __forceinline__ uint32_t factor(uint32_t e) {
-    const uint32_t f = e > 112u ? (e - 112u) << 10 : 1u << (e - 103u);
+    const uint32_t f = e > 112u ? (e - 112u) << 10 : e >= 103u ? 1u << (e - 103u) : 0u;
     return f * 0x10001u;
   }
   static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t f) {
@@ -94,7 +95,7 @@ struct Scaled<__nv_bfloat16> {
       o[2 * k] = mul(__byte_perm(size, 0, 0x4140) * sixteen + __byte_perm(sign, 0, 0x1404), f);
       o[2 * k + 1] = mul(__byte_perm(size, 0, 0x4342) * sixteen + __byte_perm(sign, 0, 0x3424), f);
     }
-    nan = (t[0] | t[1]) | (t[2] | t[3]);
+    nan |= (t[0] | t[1]) | (t[2] | t[3]);
   }
 };
 

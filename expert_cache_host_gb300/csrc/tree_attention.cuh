@@ -452,6 +452,25 @@ __device__ __forceinline__ int64_t scale_index(const Args& g, int page, int in_p
   return (((int64_t)page << (g.log2_page - g.log2_block)) + (in_page >> g.log2_block)) * g.a.cache.kv_heads + head;
 }
 
+// Rows [from, from + 32) of it, as a call: what few tiles need stays out of the loops' instructions.
+template <typename E, int HALVES, int BLOCK>
+__device__ __noinline__ uint32_t fix_v_rows(uint8_t* v, int lane, int row_shift, uint32_t pages, int left, int fresh, int from) {
+  return fix_v<E, HALVES, BLOCK>(v, lane, row_shift, pages, left, KT, fresh, from, from + 32);
+}
+
+// What convert_rows does, for any factor and any code: a lane's, one after another.
+template <typename E, int D>
+__device__ __noinline__ void convert_unusual(const uint8_t* in, uint8_t* out, uint32_t e_lo, uint32_t e_hi, int half, int lo, int hi) {
+  constexpr int COLS = D / 64;
+#pragma unroll 1
+  for (int z = 0; z < 4 * COLS * 16; ++z) {
+    const int g = z / (COLS * 16), k = z / 16 % COLS, q = z % 16;
+    const uint8_t code = in[g * 8 * D + (COLS == 2 ? (half ^ k) * 64 : 0) + q];
+    *reinterpret_cast<uint16_t*>(out + g * (8 * 128) + (COLS == 2 ? (half ^ k) * (128 * 128) : 0) + (q < 8 ? lo : hi) + (q & 7) * 2) =
+        (uint16_t)Elem<E>::pack(e4m3_value(code) * scale_of(g < 2 ? e_lo : e_hi), 0.f);
+  }
+}
+
 // One warp: 32 rows of an 8-bit tile (rows of D bytes, one after another) as
 // 16-bit numbers code * 2^(e-127) in the 128-byte swizzle layout.  A lane takes
 // 16 codes of one of 8 rows at a time; an eighth of the warp passes two rows of
@@ -470,8 +489,9 @@ __device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, u
   const int lo = ((2 * c) ^ x) * 16, hi = ((2 * c + 1) ^ x) * 16;
   auto load = [&](int g, int k) { return *reinterpret_cast<const uint4*>(in + g * 8 * D + (COLS == 2 ? (half ^ k) * 64 : 0)); };
   uint32_t nan = 0;
-  // (rolled, and without a branch: the softmax warps' code fills the instruction cache.  32 long trees, bf16: 353 us, with
-  // the loop unrolled twice 391, four times 430, and with a branch for unusual codes in it 386)
+  // (rolled, without a branch, and with the unusual in calls: the softmax warps' code fills the instruction cache.  32
+  // long trees, bf16: 325 us, with the calls inlined 352, a branch for unusual codes in the loop 386, the loop unrolled
+  // twice 391 and four times 430)
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {
     uint4 v[COLS];
@@ -488,14 +508,7 @@ __device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, u
     }
   }
   if (Scaled<E>::fast(e_lo, nan) && Scaled<E>::fast(e_hi, nan)) return;
-  // Once more where the factors or a NaN code want it.
-#pragma unroll 1
-  for (int z = 0; z < 4 * COLS * 16; ++z) {
-    const int g = z / (COLS * 16), k = z / 16 % COLS, q = z % 16;
-    const uint8_t code = in[g * 8 * D + (COLS == 2 ? (half ^ k) * 64 : 0) + q];
-    *reinterpret_cast<uint16_t*>(out + g * (8 * 128) + (COLS == 2 ? (half ^ k) * (128 * 128) : 0) + (q < 8 ? lo : hi) + (q & 7) * 2) =
-        (uint16_t)Elem<E>::pack(e4m3_value(code) * scale_of(g < 2 ? e_lo : e_hi), 0.f);
-  }
+  convert_unusual<E, D>(in, out, e_lo, e_hi, half, lo, hi);
 }
 
 template <typename E, int D, bool Q8>
@@ -676,8 +689,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
             if (kv && special(t, pages)) {
               const int left = wk.r.ctx + wk.r.n - t * KT;
               __syncwarp();
-              found |= fix_v<E, C::HALVES, C::BLOCK>(ring + st * C::TILE, lane, min(g.log2_page, 7), pages, left, KT,
-                                                     max(wk.r.ctx - t * KT, 0), first_row, first_row + 32);
+              found |= fix_v_rows<E, C::HALVES, C::BLOCK>(ring + st * C::TILE, lane, min(g.log2_page, 7), pages, left,
+                                                          max(wk.r.ctx - t * KT, 0), first_row);
               if (lane == 0) sh.nonfinite[item & 3][warp - kConverters] = found;
             }
             if (warp == kConverters && lane == 0) sh.pages[st] = pages;

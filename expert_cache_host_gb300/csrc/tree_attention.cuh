@@ -47,15 +47,15 @@
 //
 // Q8: tiles come as 8-bit codes through a ring of their own, and four more warps
 // turn them into the 16-bit tiles of the products (code * 2^(e-127), exact but for
-// f16's numbers below 2^-14; V's rows are looked over by them too).  The two
-// products, not the bytes, then bound long trees: 32 of 24..32 tokens over 8K..32K
-// keys, 0.69 GB, 0.30 TFLOP, take 385 us in bf16 and 341 in f16, where the 16-bit
-// cache takes 254 and no conversion at all took 325.  What the conversion costs is
-// the pipe of shifts, permutations and 8-bit conversions, 2 cycles a warp
-// instruction: f16 takes one conversion a pair of codes, bf16, for which there is
-// none, 3.3 such instructions and 1.3 on the multipliers' pipe (4 and more before:
-// 428 us), beside the softmax warps' own.  In shared memory a tile is written
-// twice and read twice, 1000 cycles besides the products' 1500.
+// f16's numbers below 2^-14; V's rows are looked over by them too).  The products
+// and the conversion, not the bytes, then bound long trees: 32 of 24..32 tokens
+// over 8K..32K keys, 0.69 GB, 0.30 TFLOP, take 325..331 us in bf16 and 314..324 in
+// f16, where the 16-bit cache takes 254..260.  A tile is written twice and read
+// twice in shared memory, 1000 cycles besides the products' 1500, and a warp's 32
+// rows of it take 1400 cycles in bf16 and 820 in f16: shifts, permutations and
+// 8-bit conversions share one pipe, 2 cycles a warp instruction; f16 takes one such
+// conversion for two codes, bf16, for which there is none, 3.3 such instructions
+// and 1.3 on the multipliers' pipe.
 #pragma once
 
 #include <math_constants.h>

@@ -23,9 +23,10 @@
 // and says what the cluster does next; every warp sums one stretch of the row and
 // keeps its pieces' sums, and the piece that holds the drawn point is gone through
 // once more.  Vectors come through shared memory (a thread's own, kDepth rounds
-// ahead).  One request is bound by latency, so the loop over them has no branches
-// but for unusual numbers (with them a round of 8 numbers took 2400 cycles) and its
-// code is short.
+// ahead).  64 trees of 9..17 tokens over 131072 fp32 entries take 46 us (67 MB of
+// rows; the last requests go through theirs four times), one request 9.6.  One
+// request is bound by latency, so the loop over them has no branches but for unusual
+// numbers (with them a round of 8 numbers took 2400 cycles) and its code is short.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -41,12 +42,12 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRejected = 64;
-constexpr int kUnit = 45;  // sums are in units of 2^-45
+constexpr int kUnit = 45;     // sums are in units of 2^-45
 constexpr int kNumbers = 16;  // of a thread in a round
 constexpr int kDepth = 2;     // rounds on their way
-constexpr int kResident = 2;   // CTAs of an SM
-constexpr int kPieces = 64;    // of a warp's stretch at most
-constexpr int kPiece = 4;      // rounds of a piece, or a multiple
+constexpr int kResident = 2;  // CTAs of an SM
+constexpr int kPieces = 64;   // of a warp's stretch at most
+constexpr int kPiece = 4;     // rounds of a piece, or a multiple
 
 template <typename E>
 struct Prob {  // a 16-byte vector of a row
@@ -415,10 +416,11 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
           copy(round + kDepth);
           if ((round + 1) % kPiece != 0 && round + 1 != rounds) continue;
           sum.finish(count);
-          // (the first level's number in two parts: a warp's could pass 32 bits)
+          // (in two parts each: a thread's 64 numbers stay below 2^29 and 2^28 in size, a warp's could pass 32 bits)
           const uint32_t up = __reduce_add_sync(~0u, sum.a >> 12), low = __reduce_add_sync(~0u, sum.a & 0xFFFu);
-          const int32_t rest = __reduce_add_sync(~0u, (int32_t)sum.b);
-          piece_sum += ((((uint64_t)up << 12) + low) << (kUnit - 22)) + (int64_t)rest;
+          const int32_t b = (int32_t)sum.b;
+          const int32_t b_up = __reduce_add_sync(~0u, b >> 12), b_low = __reduce_add_sync(~0u, b & 0xFFF);
+          piece_sum += ((((uint64_t)up << 12) + low) << (kUnit - 22)) + (((int64_t)b_up << 12) + b_low);
           size += (float)up * 0x1p-10f;
           sum = Levels();
           count = 0;

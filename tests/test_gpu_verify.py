@@ -145,6 +145,20 @@ def test_flat_and_peaked_rows(ft):
             Case(ft, [12] * 30, 8192, "f32", True, draft, seed=5, sharp=sharp).run()
 
 
+@pytest.mark.parametrize("V", [3001, 50021, 131071, 200003])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_equal_probabilities(ft, V, dtype):
+    """Every entry the same, no multiple of a power of two: what is left of the entries at any level adds up."""
+    for draft in (False, True):
+        c = Case(ft, [1] * 30 + [2] * 30, V, dtype, False, draft, seed=V, sharp=0.0)
+        c.p.fill_(1.0 / V)
+        c.u.fill_(0.999)
+        if draft:
+            c.q.fill_(0.4 / V)
+            c.q[:, ::2] = 1.5 / V
+        c.run()
+
+
 def test_many_rows_and_many_children(ft):
     """More rows than are gathered ahead, and a row with many children that are all rejected."""
     c = Case(ft, [900, 60], 500, "f32", True, True, seed=6)

@@ -36,8 +36,9 @@ EXPORTS = (
     "ft_ratio_adapter_init", "ft_ratio_adapter_update", "ft_report_host_rate", "ft_measured_bandwidths",
     "ft_adapt_ratio", "ft_decode_meters", "ft_decode_path",
     "ft_kv_plan", "ft_qk_norm_rope", "ft_tree_attention", "ft_tree_attention_workspace", "ft_token_logprobs",
-    "ft_last_error",
+    "ft_verify_drafts", "ft_last_error",
 )
+EXPORTS_KV8 = ("ft_kv8_store", "ft_kv8_load", "ft_kv8_attention", "ft_kv8_attention_workspace")
 FT_K_ROUTE, FT_K_CONTROL, FT_K_FILL, FT_K_EXPERTS, FT_K_MERGE, FT_K_UPLOAD, FT_K_PREFILL, FT_K_GEMM, FT_K_CPU = range(9)
 FT_K_COUNT = 9
 KERNEL_CLASSES = ("route", "control", "fill", "experts", "merge", "upload", "prefill", "gemm", "cpu")

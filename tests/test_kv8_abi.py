@@ -157,6 +157,18 @@ def test_struct_sizes_match_the_header():
     assert got == want
 
 
+def test_every_declared_symbol_is_exported():
+    """Names with a digit too."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "ft_moe.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(ft_[a-z0-9_]+)\s*\(", src))
+    assert names == set(ft.EXPORTS) | set(ft.EXPORTS_KV8)
+    for n in names:
+        assert hasattr(ft.load(), n), n
+
+
 def test_reference_codes():
     """The reference rounds to the nearest of all 253 numbers, ties to the even code."""
     codes = np.arange(256, dtype=np.uint8)

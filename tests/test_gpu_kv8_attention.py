@@ -491,3 +491,53 @@ def test_back_to_back(ft, new):
     torch.cuda.synchronize()
     for a, (out, lse) in zip(batch, want):
         assert torch.equal(a.out, out) and torch.equal(a.lse, lse) and a.status.item() == 0
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P,block", [
+    # up to 16 rows a key head: 2 x 8, 1 x 16, 5 x 3, 1 x 9, 16 x 1
+    ([2000, 40, 0], [2, 1, 2], 32, 4, 128, "bf16", 16, 16), ([700, 17], [1, 1], 32, 2, 128, "f16", 64, 32),
+    ([1300, 3], [5, 4], 6, 2, 128, "bf16", 32, 16), ([130], [1], 9, 1, 64, "bf16", 16, 16),
+    ([400, 5, 64], [16, 3, 16], 2, 2, 128, "f16", 128, 128), ([9000], [2], 64, 8, 64, "f16", 64, 64)])
+@pytest.mark.parametrize("mask", ["chain", "random"])
+def test_rows_up_to_sixteen(ft, ctx, new, Hq, Hkv, D, dtype, P, block, mask):
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, block, mask=mask, seed=Hq + D).run()
+    a.check()
+    assert a.status.item() == 0
+
+
+@pytest.mark.parametrize("code,byte", [(0x7F, 127), (0x7E, 254), (0xFE, 200), (0x38, 255), (0xFF, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq", [4, 16, 32])
+def test_a_later_token_in_a_block_of_its_own(ft, code, byte, dtype, Hq):
+    """Whatever its codes and scales, the rows before it do not see it: with 4, 16 and 32 rows a key head."""
+    a = Attn(ft, [15, 47], [2, 2], Hq, 2, 128, dtype, 32, 16, mask="chain", seed=3).run()
+    a.check()
+    clean = a.out.clone()
+    for b in range(2):
+        page, row = a.rows[b][0][a.ctx[b] + 1], a.rows[b][1][a.ctx[b] + 1]
+        for kv in range(2):
+            a.codes[kv][page, row] = code
+            a.bytes[kv][page, row // 16] = byte
+    a.run()
+    assert torch.equal(a.out[[0, 2]], clean[[0, 2]])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [[1, 1], [3, 9]])
+def test_blocks_of_zeros_and_blocks_far_larger(ft, dtype, new):
+    """Keys or values all zero with byte 0, and values 2^12 larger than the others' with next to no weight: the scores'
+    share of both stays."""
+    a = Attn(ft, [500, 70], new, 8, 2, 128, dtype, 16, 16, mask="chain", seed=21)
+    for b in range(2):
+        page = a.rows[b][0][:64:16]  # the request's first four blocks
+        a.codes[1][page[0]], a.bytes[1][page[0]] = 0, 0
+        a.codes[0][page[1]], a.bytes[0][page[1]] = 0, 0
+        a.bytes[1][page[2]] += 12
+        # scores near -40: keys along minus the queries' sum, which is what every row shares here
+        a.q[a.start[b]:a.start[b + 1]] = a.q[a.start[b], 0]
+        away = -a.q[a.start[b], 0].float()
+        x = away * (40.0 / a.scale / float((away * away).sum()))
+        e = int(torch.ceil(torch.log2(x.abs().max() / 448)).item())
+        a.codes[0][page[2]] = (x * 2.0 ** -e).to(torch.float8_e4m3fn).view(torch.uint8)
+        a.bytes[0][page[2]] = 127 + e
+    a.run().check()

@@ -460,7 +460,8 @@ __device__ __noinline__ uint32_t fix_v_rows(uint8_t* v, int lane, int row_shift,
 
 // What convert_rows does, for any factor and any code: a lane's, one after another.
 template <typename E, int D>
-__device__ __noinline__ void convert_unusual(const uint8_t* in, uint8_t* out, uint32_t e_lo, uint32_t e_hi, int half, int lo, int hi) {
+__device__ __noinline__ void convert_unusual(const uint8_t* in, uint8_t* out, uint32_t e_lo, uint32_t e_hi, int half, int lo,
+                                             int hi) {
   constexpr int COLS = D / 64;
 #pragma unroll 1
   for (int z = 0; z < 4 * COLS * 16; ++z) {

@@ -541,3 +541,24 @@ def test_blocks_of_zeros_and_blocks_far_larger(ft, dtype, new):
         a.codes[0][page[2]] = (x * 2.0 ** -e).to(torch.float8_e4m3fn).view(torch.uint8)
         a.bytes[0][page[2]] = 127 + e
     a.run().check()
+
+
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,P,block", [
+    ([33000] * 8, [1] * 8, 16, 8, 128, "bf16", 16, 16), ([40000] * 7 + [13], [2] * 8, 8, 8, 64, "f16", 128, 64),
+    ([33000] * 6 + [17], [3] * 7, 64, 8, 128, "bf16", 64, 32)])
+def test_many_tiles_to_a_cta(ft, ctx, new, Hq, Hkv, D, dtype, P, block):
+    """More tiles than a window of pages holds, one and two windows on."""
+    a = Attn(ft, ctx, new, Hq, Hkv, D, dtype, P, block, seed=D).run()
+    a.check()
+    a.table[1, 1000 // (P // 16)] = -1  # a page missing far inside
+    a.status.zero_()
+    clean = a.out.clone()
+    a.run()
+    assert a.status.item() == ft.FT_ST_BAD_SLOT
+    lo = 1000 // (P // 16) * P
+    keep = [i for i in range(a.ctx[1] + a.new[1]) if not lo <= i < lo + P]
+    a.rows[1] = tuple(x[keep] for x in a.rows[1])
+    a.ctx[1] -= P
+    a.check()
+    first = a.start[1]
+    assert torch.equal(a.out[:first], clean[:first])

@@ -560,26 +560,12 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
 }
 
 template <typename E, int CS>
-cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
-  static thread_local int configured = -1;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (configured != dev) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
-    if (e != cudaSuccess) return e;
-    if (CS > 8) {
-      const cudaError_t e2 = cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e2 != cudaSuccess) return e2;
-    }
-    configured = dev;
-  }
-  cudaLaunchConfig_t cfg{};
+void configure(const ft_verify_args& a, cudaStream_t st, cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
+  cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3((unsigned)a.num_reqs * CS);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -587,17 +573,58 @@ cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CS > 1 ? 2 : 1;
+}
+
+template <typename E, int CS>
+cudaError_t prepare() {
+  static thread_local int configured = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured == dev) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+  if (e == cudaSuccess && CS > 8)
+    e = cudaFuncSetAttribute(verify_drafts_kernel<E, CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) configured = dev;
+  return e;
+}
+
+template <typename E, int CS>
+cudaError_t launch(const ft_verify_args& a, cudaStream_t st) {
+  if (const cudaError_t e = prepare<E, CS>()) return e;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  configure<E, CS>(a, st, cfg, attr);
   return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<E, CS>, a);
+}
+
+// Clusters of kMaxCluster CTAs that run at once (0 where there are none).
+template <typename E>
+int room(const ft_verify_args& a) {
+  static thread_local int known_dev = -1, clusters = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev != known_dev) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    configure<E, kMaxCluster>(a, nullptr, cfg, attr);
+    if (prepare<E, kMaxCluster>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, verify_drafts_kernel<E, kMaxCluster>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      clusters = 0;
+    }
+    known_dev = dev;
+  }
+  return clusters;
 }
 
 template <typename E>
 cudaError_t launch_cs(const ft_verify_args& a, cudaStream_t st) {
-  // As many CTAs a request as run at once, while a lane has more than one vector of a row.  A cluster lies in one GPC, so
-  // of 16 CTAs there is room for two on every 18 SMs (16 requests of 131072 entries: 17.5 us with 16, 22.3 with 8; with a
-  // cluster more than there is room for, 37 requests of 50021 16-bit entries took 23 us, with 8 CTAs each 18).
+  // As many CTAs a request as run at once, while a lane has more than one vector of a row.  A cluster lies in one GPC, and
+  // of 16 CTAs there is room for 14; a few more wait for the first to end (16 requests' trees of 131072 entries: 17.2 us
+  // with 16, 22.2 with 8; 37 requests of 50021 16-bit entries 23 us, with 8 CTAs each 18).
   int cs = 1;
   while (cs < kMaxCluster && a.V / Prob<E>::N / cs > kThreads &&
-         (cs < 8 ? (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident : (int64_t)a.num_reqs * 9 <= sm_count()))
+         (cs < 8 ? (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident : a.num_reqs * 4ll <= room<E>(a) * 5ll))
     cs *= 2;
   switch (cs) {
     case 1: return launch<E, 1>(a, st);

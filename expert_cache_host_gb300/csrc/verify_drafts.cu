@@ -12,7 +12,7 @@
 // The token is a whole number next to borders of the running sum: fp32 sums over
 // 131072 entries would move the borders by more than many entries are wide, and
 // 64-bit floating point runs at a sixty-fourth of the rate.  So entries are cut into
-// whole numbers at two levels (multiples of 2^-22 and 2^-45; adding a constant
+// whole numbers at two levels (multiples of 2^-22 and 2^-44; adding a constant
 // leaves each level's number in the sum's low bits) and added as such: sums do not
 // depend on their order.  After k rejections
 //   a = max(p - q B, 0),  B = 1 + A_1 + .. + A_(k-1)
@@ -42,7 +42,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRejected = 64;
-constexpr int kUnit = 45;     // sums are in units of 2^-45
+constexpr int kUnit = 44;     // sums are in units of 2^-44
 constexpr int kNumbers = 16;  // of a thread in a round
 constexpr int kDepth = 2;     // rounds on their way
 constexpr int kResident = 2;  // CTAs of an SM
@@ -77,11 +77,15 @@ __device__ __forceinline__ bool in_range(float v) { return v >= 0.f && v <= 2.f;
 // A random number as it is used.
 __device__ __forceinline__ float below_one(float u) { return u > 0.f ? fminf(u, 0.99999994f) : 0.f; }
 
-// Sums of pairs of numbers hi + lo in [0, 2] (|lo| <= 2^-24 hi) as whole numbers at
-// two levels; each counts the constants' bits once a number.
+// Sums of pairs of numbers hi + lo in [0, 2], hi the fp32 number next to the pair
+// (|lo| <= 2^-24), as whole numbers at two levels; each counts the constants' bits
+// once a number.  The first level leaves at most 2^-23 of hi, so that the second
+// takes less than 2^-22 in size: kB and it stay in one binade, whose numbers are
+// 2^-44 apart.  (With 0x1.8p-22 and 2^-45 there is room for 2^-23 alone: where lo
+// came on top, after a rejection, entries were off by up to 2^-24.)
 struct Levels {
   uint32_t a = 0, b = 0;
-  static constexpr float kA = 2.f, kB = 0x1.8p-22f;
+  static constexpr float kA = 2.f, kB = 0x1.8p-21f;
   __device__ __forceinline__ void add(uint64_t hi, uint64_t lo) {
     const uint64_t minus = pair2(-1.f, -1.f);
     const uint64_t s = add2(hi, pair2(kA, kA));
@@ -385,9 +389,10 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
           const uint64_t f = pair2(q[2 * i], q[2 * i + 1]), t = mul2(f, mh);  // q B = -t + e
           const uint64_t e = fma2(f, bl, fma2(f, bh, t));
           const uint64_t d = add2(hi[i], t);
-          const uint64_t l = fma2(e, minus, add2(fma2(d, minus, hi[i]), t));  // d + l = p - q B, exactly where p >= q B / 2
-          const float2 x = split2(d), y = split2(l), z = split2(add2(d, l));
-          hi[i] = pair2(z.x > 0.f ? x.x : 0.f, z.y > 0.f ? x.y : 0.f);
+          const uint64_t l = fma2(e, minus, add2(fma2(d, minus, hi[i]), t));  // d + l = p - q B, l rounded
+          const uint64_t s = add2(d, l);  // and the number next to it: l holds both roundings above, up to 2^-22 where p > 1
+          const float2 z = split2(s), y = split2(fma2(fma2(d, minus, s), minus, l));
+          hi[i] = pair2(z.x > 0.f ? z.x : 0.f, z.y > 0.f ? z.y : 0.f);
           lo[i] = pair2(z.x > 0.f ? y.x : 0.f, z.y > 0.f ? y.y : 0.f);
         }
       }
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
         bad = true;
       }
       if (command == kSum) {
-        w.A = (double)total * 0x1p-45;
+        w.A = (double)total * (1.0 / (1ull << kUnit));
         w.known = true;
         break;
       }

@@ -773,7 +773,8 @@ int ft_kv8_attention_workspace(const ft_kv8_attn_args* args, uint64_t* bytes);
  *              accepted[q_start[b]] on, then -1
  *   n_accepted [num_reqs], next_token [num_reqs]
  * Rows whose parent is no row of theirs take no part.  Sums are of whole
- * multiples of 2^-45 to which entries are rounded, so results do not depend on any
+ * multiples of 2^-44 to which entries are rounded (what a rejection with draft
+ * probabilities leaves of one to within 2^-44), so results do not depend on any
  * order.  An entry
  * outside [0, 2] counts as 0; it is reported (FT_ST_NAN) where it is met, and so is
  * a row with nothing to draw from or a sum above 8 of what is drawn from: next_token

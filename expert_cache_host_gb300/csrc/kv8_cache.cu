@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 4) kv8_store_kernel(const __grid_con
     for (int i = 0; i < kSteps; ++i) {
       const int row = row0 + i * RPS;
       x[i] = make_uint4(0, 0, 0, 0);
-      if (active && row >= lo && row < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + row) * stride));
+      if (active && row >= lo && row < hi) x[i] = *reinterpret_cast<const uint4*>(src + (t0 + row) * stride);
     }
   }
   const bool there = page >= 0 && page < a.cache.num_pages;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) kv8_load_kernel(const __grid_constan
   const int64_t token_stride = values ? a.cache.v_token_stride : a.cache.k_token_stride;
   int64_t slot[kItems];
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) slot[i] = t0 + i < a.T ? __ldg(a.slots + t0 + i) : -1;
+  for (int i = 0; i < kItems; ++i) slot[i] = t0 + i < a.T ? a.slots[t0 + i] : -1;
   uint4 c[kItems];
   uint32_t e[kItems];
 #pragma unroll

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, NB>::CTAS)) few_rows_kernel(
     auto bytes_at = [&](int first, int pg) -> uint32_t {
       if (pg < 0) return kNone;
       const int64_t at = tree_attention::scale_index(g, pg, ((first + lane) * KT + warp * kChunk) & page_mask, wk.h);
-      return __ldg(g.k_scale + at) | (uint32_t)__ldg(g.v_scale + at) << 8;
+      return g.k_scale[at] | (uint32_t)g.v_scale[at] << 8;
     };
     int page = page_at(wk.t0), page_next = -1;
     uint32_t bytes = bytes_at(wk.t0, page), bytes_next = kNone;

@@ -47,7 +47,10 @@ __device__ __forceinline__ void proxy_fence_writes() { asm volatile("fence.proxy
 // depends on (the previous kernel in the stream, when launched with
 // programmatic stream serialization) has completed and its writes are
 // visible; a no-op otherwise.  pdl_trigger: let the dependent grid launch now
-// (it still waits with pdl_wait before using this grid's results).
+// (it still waits with pdl_wait before using this grid's results).  What another
+// grid of the stream may write is read by plain loads: ld.global.nc (__ldg) takes it
+// as constant from this grid's start, which lies before the wait, and may be moved
+// there.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

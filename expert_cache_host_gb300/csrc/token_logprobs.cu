@@ -162,7 +162,7 @@ struct Logit<float> {
                          fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
     return m;
   }
-  static __device__ __forceinline__ float scalar(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float scalar(const float* p) { return *p; }
 };
 template <typename E, typename E2>
 struct Logit16 {
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
   // past the end: the batch's first vector again, left out of the sums
   auto load = [&](int v) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) raw[i] = __ldg(body + (v + i * kThreads < v1 ? v + i * kThreads : v));
+    for (int i = 0; i < kVecs; ++i) raw[i] = __ldcg(body + (v + i * kThreads < v1 ? v + i * kThreads : v));
   };
   if (v0 + tid < v1) load(v0 + tid);
   for (int v = v0 + tid; v < v1; v += kThreads * kVecs) {
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
 #pragma unroll 1
       for (int i = 0; i < kVecs && i < left; ++i) {
         float x[N];
-        L::unpack(__ldg(body + v + i * kThreads), x);
+        L::unpack(body[v + i * kThreads], x);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           nan |= x[j] != x[j];
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
 #pragma unroll 2
       for (int v = first + lane * kThreads; v < v1; v += 32 * kThreads) {
         float x[N];
-        L::unpack(__ldg(body + v), x);
+        L::unpack(body[v], x);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           if (!(x[j] < bound)) {  // NaN too: it counts as -inf, which may be the bound
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(const ft_lo
       uint64_t top = w == 0 ? warp_sort(edge, lane) : 0;
       for (int v = v0 + w * 32; v < v1; v += kThreads) {
         float x[N];
-        if (v + lane < v1) L::unpack(__ldg(body + v + lane), x);
+        if (v + lane < v1) L::unpack(body[v + lane], x);
         const uint64_t cut = __shfl_sync(~0u, top, a.top_n - 1);
 #pragma unroll
         for (int j = 0; j < N; ++j) {

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::THREADS, 1)
       const int row = (lane & 7) << g.log2_block;
       if (lane < 16 || page < 0 || page >= a.cache.num_pages || t >= wk.t1 || t * KT + row >= wk.r.ctx + wk.r.n) return 0;
       const uint8_t* s = lane & 8 ? g.v_scale : g.k_scale;
-      return __ldg(s + scale_index(g, page, (t * KT + row) & ((1 << g.log2_page) - 1), wk.h));
+      return s[scale_index(g, page, (t * KT + row) & ((1 << g.log2_page) - 1), wk.h)];
     };
     auto used = [&](int t) { return lane < per_tile && t * KT + lane * box_rows < wk.r.ctx + wk.r.n; };
     auto there = [&](int t, int page) { return used(t) && page >= 0 && page < a.cache.num_pages; };

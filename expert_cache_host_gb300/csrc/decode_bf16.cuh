@@ -36,11 +36,11 @@ __device__ __forceinline__ float dot8h(const uint4 w, const float4 h0, const flo
   return s;
 }
 
-// 16-byte read-only load kept where it is written (not sunk past the branches
-// that follow), so that it overlaps the loads issued after it.
-__device__ __forceinline__ uint4 ld_nc_early(const uint4* p) {
+// 16-byte load kept where it is written (not sunk past the branches that
+// follow), so that it overlaps the loads issued after it.
+__device__ __forceinline__ uint4 ld_early(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;

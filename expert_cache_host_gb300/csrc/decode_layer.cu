@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
     for (int j = 0; j < kXPre; ++j) {
       const int i = tid + j * kConsumers;
-      if (i < d / 8) xpre[j] = ld_nc_early(src + i);
+      if (i < d / 8) xpre[j] = ld_early(src + i);
     }
   }
   // work lists: warp 0 splits the groups into resident and installed, in order,

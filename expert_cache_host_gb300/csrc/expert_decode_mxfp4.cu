@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int j = 0; j < kXPre; ++j) {
       const int i = tid + j * kConsumers;
-      if (i < d / 8) xpre[j] = ld_nc_early(src + i);
+      if (i < d / 8) xpre[j] = ld_early(src + i);
     }
   }
   // Fetch every per-group value at once (one memory round trip before the

@@ -22,9 +22,8 @@ constexpr int kUn = 8;     // loads in flight per lane
 constexpr int kRun = 8;    // rows per run of the final sum
 
 __global__ void __launch_bounds__(kCols* kRows)
-    merge_kernel(const float4* __restrict__ ypart, int n_chunks, const int32_t* __restrict__ slot_ids,
-                 const float* __restrict__ w, const float4* __restrict__ partial, float4* __restrict__ out, int k,
-                 int d4) {
+    merge_kernel(const float4* ypart, int n_chunks, const int32_t* slot_ids, const float* w, const float4* partial,
+                 float4* out, int k, int d4) {
   __shared__ float4 red[kRows][kCols];
   // the next kernel (the next layer's routing) may start now; this one waits
   // for the experts' partial sums
@@ -48,8 +47,8 @@ __global__ void __launch_bounds__(kCols* kRows)
           // the three loads are independent (ypart is allocated for every
           // route); a route without a slot then contributes exactly nothing
           const int j = p / n_chunks, c = p - j * n_chunks, r = t * k + j;
-          const int sid = __ldg(slot_ids + r);
-          const float wr = __ldg(w + r);
+          const int sid = slot_ids[r];
+          const float wr = w[r];
           const float4 y = ypart[((size_t)r * n_chunks + c) * d4 + i];
           if (sid >= 0) {
             wv[u] = wr;

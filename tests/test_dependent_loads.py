@@ -31,13 +31,14 @@ def waiting():
 
 ATTENTION_SIDE = ["kv8_cache.cu", "kv8_few.cuh", "kv_plan.cu", "qk_norm_rope.cu", "token_logprobs.cu", "tree_attention.cuh",
                   "verify_drafts.cu"]
+EXPERTS = ["control.cu", "decode_bf16.cuh", "expert_decode.cu", "expert_decode_mxfp4.cu", "merge.cu"]
 
 
 def test_these_kernels_wait():
-    assert set(ATTENTION_SIDE) <= set(waiting())
+    assert set(ATTENTION_SIDE + EXPERTS) - {"decode_bf16.cuh"} == set(waiting())
 
 
-@pytest.mark.parametrize("name", ATTENTION_SIDE)
+@pytest.mark.parametrize("name", ATTENTION_SIDE + EXPERTS)
 def test_non_coherent_loads_are_of_constants(name):
     text = code(os.path.join(CSRC, name))
     assert len(re.findall(r"__ldg\(|ld\.global\.nc", text)) == CONSTANTS.get(name, 0)

@@ -19,8 +19,9 @@
 //   p = 2^(c (X - M)), l += p          and      P = 2^(c (X - M) + ev - mo + 11)
 // P in f16, where mo follows the maximum of c (X - M) + ev, so that a value's
 // weight is held relative to the largest weight times scale.  Queries are f16 too,
-// bf16 ones times a power of two of their row (the largest becomes 2^10: numbers
-// below 2^-34 of it are rounded to multiples of 2^-35).
+// bf16 ones times a power of two of their row.  The largest lies in [2^10, 2^11)
+// then, where f16 holds all 8 bits of a bf16 number from 2^-17 on: numbers below
+// 2^-27 of the row's largest are rounded to multiples of at most 2^-34 of it.
 //
 // A CTA's eight warps take the eight chunks of a 128-key tile, each with a ring of
 // its own (TMA) and no barrier of the CTA before an item's end, where they are

@@ -476,8 +476,8 @@ __device__ __noinline__ void convert_unusual(const uint8_t* in, uint8_t* out, ui
 // 16-bit numbers code * 2^(e-127) in the 128-byte swizzle layout.  A lane takes
 // 16 codes of one of 8 rows at a time; an eighth of the warp passes two rows of
 // half their columns each, so that neither the loads nor the stores meet in a
-// bank.  The rows lie in two blocks at most: `bytes`, whose first 16 and last 16
-// rows' are warp-uniform.
+// bank.  The rows lie in two blocks at most: e_lo is the scale byte of the first 16,
+// e_hi that of the last 16 (both warp-uniform).
 template <typename E, int D>
 __device__ __forceinline__ void convert_rows(const uint8_t* src, uint8_t* dst, uint32_t e_lo, uint32_t e_hi, int lane,
                                              uint32_t sixteen, uint32_t one) {

@@ -720,7 +720,11 @@ int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
  * be rounded to dtype before the products, which keeps what ft_kv8_store wrote
  * from it (of f16, numbers below 2^-14 have its fixed spacing of 2^-24); one past
  * dtype's range may then count as infinite.  NaN codes and scale bytes of 255 are
- * NaN.
+ * NaN.  Where max_new * (q_heads / kv_heads) is at most 16 the cache's numbers are
+ * not rounded, but in either dtype a probability times its value's scale is, to f16
+ * (below 2^-25 of the row's largest to multiples of 2^-35 of it), and so are the
+ * numbers of a bf16 query below 2^-27 of its head's largest (to multiples of at most
+ * 2^-34 of it).
  * max_new: no request has more new tokens than this (0: max_tokens); one that has
  * is reported (FT_ST_NO_ROOM) and its rows are not written.  A small max_new lets
  * short rows take a kernel of their own.  workspace:

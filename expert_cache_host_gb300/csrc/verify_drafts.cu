@@ -43,6 +43,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kRejected = 64;
 constexpr int kUnit = 44;     // sums are in units of 2^-44
+constexpr double kUnits = 1ull << kUnit;
 constexpr int kNumbers = 16;  // of a thread in a round
 constexpr int kDepth = 2;     // rounds on their way
 constexpr int kResident = 2;  // CTAs of an SM
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
           w.B += w.A;
           // without draft probabilities the next A is known once one sum is
           w.known = w.k > 0 && !a.draft_probs;
-          if (w.known) w.A -= left;
+          if (w.known) w.A -= rint(left * kUnits) / kUnits;  // (as it was added)
           ++w.k;
         }
       }
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_drafts_kernel(cons
         bad = true;
       }
       if (command == kSum) {
-        w.A = (double)total * (1.0 / (1ull << kUnit));
+        w.A = (double)total / kUnits;
         w.known = true;
         break;
       }

@@ -72,8 +72,8 @@ def least(a, u):
 class Batch:
     """Requests of a first row and children of it, every one of k + `extra` tokens."""
 
-    def __init__(self, dtype, V):
-        self.dtype, self.V = dtype, V
+    def __init__(self, dtype, V, draft=True):
+        self.dtype, self.V, self.draft = dtype, V, draft
         self.p, self.q, self.tokens, self.u, self.draw, self.n, self.want = [], [], [], [], [], [], []
 
     def add(self, p, q, tokens, u, draw, accepted, token):
@@ -96,7 +96,7 @@ class Batch:
         accepted, count, token, status = (torch.full((n,), v, dtype=i32, device="cuda") for n, v in ((T, -7), (B, -7), (B, -7), (1, 0)))
         code = {"bf16": ft.FT_DTYPE_BF16, "f16": ft.FT_DTYPE_F16, "f32": ft.FT_DTYPE_F32}[self.dtype]
         ft.ft_verify_drafts(ft.make_verify_args(
-            probs=p.data_ptr(), draft_probs=q.data_ptr(), tokens=d[0].data_ptr(), parents=d[1].data_ptr(),
+            probs=p.data_ptr(), draft_probs=q.data_ptr() if self.draft else 0, tokens=d[0].data_ptr(), parents=d[1].data_ptr(),
             accept_u=d[2].data_ptr(), draw_u=d[3].data_ptr(), q_start=d[4].data_ptr(), accepted=accepted.data_ptr(),
             n_accepted=count.data_ptr(), next_token=token.data_ptr(), status=status.data_ptr(), probs_stride=self.V,
             draft_stride=self.V, dtype=code, max_tokens=T, num_reqs=B, V=self.V), torch.cuda.current_stream().cuda_stream)
@@ -188,4 +188,32 @@ def test_later_children_on_both_sides_of_acceptance(ft, k, V, dtype, most):
             if abs(off) * fq[x] * A > 2 * MARGIN and u < 1:
                 b.add(p, q, tokens + [x], [ONE] * k + [u], 0.0, k + 1 if off < 0 else -1, None)
     assert len(b.n) > 30, len(b.n)
+    b.check(ft)
+
+
+def whole(x):
+    """x rounded to a multiple of 2^-44, ties to even."""
+    return Fraction(round(x * 2 ** 44), 2 ** 44)
+
+
+@pytest.mark.parametrize("removed,x,other,u", [
+    (["0x1.36f676p-24", "0x1.6f0368p-24", "0x1.3d9c18p-27"], "0x1.0f21dep-24", "0x1.fb17c4p-27", "0x1.9efbaap-1"),
+    (["0x1.24ede6p-24", "0x1.922766p-25", "0x1.1a61dcp-25"], "0x1.5f5572p-24", "0x1.6c99c8p-24", "0x1.f68324p-2"),
+    (["0x1.907a70p-25", "0x1.7f1506p-27", "0x1.c6f878p-27"], "0x1.95e762p-23", "0x1.7242a6p-25", "0x1.a0ec18p-1"),
+    (["0x1.3f98e2p-25", "0x1.b2f14cp-25", "0x1.14f474p-26"], "0x1.867348p-23", "0x1.7579dap-24", "0x1.5a5a36p-1"),
+    (["0x1.49b64ap-24", "0x1.1e3990p-27", "0x1.2a3af4p-26"], "0x1.26e876p-23", "0x1.afd1b2p-25", "0x1.76ccbcp-1")])
+def test_little_left_without_draft_probabilities(ft, removed, x, other, u):
+    """Nearly all of a row is rejected, then three of the small entries: what is left is the sum of the other entries,
+    each rounded, not what the removed ones as they are leave of the sum before."""
+    removed, x, other = [float.fromhex(r) for r in removed], float.fromhex(x), float.fromhex(other)
+    p, u = [0.99, *removed, x, other], np.float32(float.fromhex(u))
+    a, left = [Fraction(y) for y in p], Fraction(0)
+    for j in range(4):  # tokens 0 .. 3 are rejected
+        A = sum(whole(y) for y in a[j:]) if j else Fraction(1)
+        assert Fraction(float(ONE)) * A > a[j]
+    A = whole(a[4]) + whole(a[5])
+    b = Batch("f32", 6, draft=False)
+    for v in (u, np.nextafter(u, np.float32(0)), np.nextafter(u, np.float32(1))):
+        b.add(p, p, [0, 1, 2, 3, 4], [ONE] * 4 + [v], 0.0, 5 if Fraction(float(v)) * A < a[4] else -1, None)
+    assert {w[0] for w in b.want} == {5, -1}
     b.check(ft)

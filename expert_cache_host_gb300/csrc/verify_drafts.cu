@@ -23,7 +23,7 @@
 // and says what the cluster does next; every warp sums one stretch of the row and
 // keeps its pieces' sums, and the piece that holds the drawn point is gone through
 // once more.  Vectors come through shared memory (a thread's own, kDepth rounds
-// ahead).  64 trees of 9..17 tokens over 131072 fp32 entries take 46 us (67 MB of
+// ahead).  64 trees of 9..17 tokens over 131072 fp32 entries take 43..50 us (67 MB of
 // rows; the last requests go through theirs four times), one request 9.6.  One
 // request is bound by latency, so the loop over them has no branches but for unusual
 // numbers (with them a round of 8 numbers took 2400 cycles) and its code is short.
@@ -626,8 +626,10 @@ int room(const ft_verify_args& a) {
 template <typename E>
 cudaError_t launch_cs(const ft_verify_args& a, cudaStream_t st) {
   // As many CTAs a request as run at once, while a lane has more than one vector of a row.  A cluster lies in one GPC, and
-  // of 16 CTAs there is room for 14; a few more wait for the first to end (16 requests' trees of 131072 entries: 17.2 us
-  // with 16, 22.2 with 8; 37 requests of 50021 16-bit entries 23 us, with 8 CTAs each 18).
+  // of 16 CTAs there is room for 14; a few more wait for the first to end.  Three batches each of trees over 131072 fp32
+  // entries, in us: 16 requests 18, 17, 25 with 16 CTAs and 24, 21, 31 with 8; 17 requests 25, 37, 37 and 22, 36, 39; 18
+  // requests 24, 29, 35 and 24, 33, 33.  Rows of 50021 16-bit entries: 14 requests 16, 14, 13 and 16, 14, 14; 16 requests
+  // 16, 17, 19 and 14, 14, 15; 37 requests 23 and 18.
   int cs = 1;
   while (cs < kMaxCluster && a.V / Prob<E>::N / cs > kThreads &&
          (cs < 8 ? (int64_t)a.num_reqs * cs * 2 <= (int64_t)sm_count() * kResident : a.num_reqs * 4ll <= room<E>(a) * 5ll))

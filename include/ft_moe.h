@@ -595,8 +595,8 @@ typedef struct ft_attn_args {
 } ft_attn_args;
 int ft_tree_attention(const ft_attn_args* args, void* stream);
 
-/* Workspace bytes for ft_tree_attention with these args (pointers are not
- * looked at).  The head size and the GPU's number of SMs decide, whatever the
+/* Workspace bytes for ft_tree_attention with these args (pointers other than the
+ * cache's are not looked at).  The head size and the GPU's number of SMs decide, whatever the
  * batch: two partial outputs of 256 rows an SM, about 40 MB at head_dim 128 on
  * 152 SMs, so that one workspace serves every call of a stream. */
 int ft_tree_attention_workspace(const ft_attn_args* args, uint64_t* bytes);
@@ -726,8 +726,11 @@ int ft_kv8_load(const ft_kv8_load_args* args, void* stream);
  * numbers of a bf16 query below 2^-27 of its head's largest (to multiples of at most
  * 2^-34 of it).
  * max_new: no request has more new tokens than this (0: max_tokens); one that has
- * is reported (FT_ST_NO_ROOM) and its rows are not written.  A small max_new lets
- * short rows take a kernel of their own.  workspace:
+ * is reported (FT_ST_NO_ROOM) and its rows are not written.  With at most 16 rows a
+ * key head (max_new * (q_heads / kv_heads)) a call takes a kernel that reads the codes
+ * into registers; with more, all of its requests, single tokens too, go through tiles
+ * that are converted to 16 bits first, which takes single tokens twice as long: give
+ * single tokens and long chunks calls of their own.  workspace:
  * ft_kv8_attention_workspace bytes, 16-byte aligned, any contents; calls that may
  * overlap on the GPU need one each. */
 typedef struct ft_kv8_attn_args {
@@ -754,8 +757,8 @@ typedef struct ft_kv8_attn_args {
 } ft_kv8_attn_args;
 int ft_kv8_attention(const ft_kv8_attn_args* args, void* stream);
 
-/* Workspace bytes for ft_kv8_attention with these args (pointers are not looked
- * at): the head size and the GPU's number of SMs decide. */
+/* Workspace bytes for ft_kv8_attention with these args (pointers other than the
+ * cache's are not looked at): the head size and the GPU's number of SMs decide. */
 int ft_kv8_attention_workspace(const ft_kv8_attn_args* args, uint64_t* bytes);
 
 /* Which drafted tokens of a step stay, and the token that follows them, from the
